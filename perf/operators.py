@@ -80,7 +80,7 @@ def draw(rng):
         E = _spread(rng, 2, 256)
         k = rng.randrange(1, min(E, 12) + 1)
         if op != "router_bwd":
-            T = max(1, min(T, 13312 // wide // k))
+            T = max(1, min(T, 11264 // wide // k))
         kw.update(E=E, k=k, zipf=rng.random() < 0.5, drop=rng.choice([0.0, 0.0, 0.1, 0.5]))
         kw["ydtype"] = rng.choice([kw["dtype"], "f32"])
         if op == "router_bwd":
