@@ -231,6 +231,126 @@ int moe_bf16_layer(const uint16_t* x_bf16, const uint16_t* logits_bf16,
                    void* workspace, size_t workspace_bytes,
                    uint16_t* out_bf16, int flags, moe_stream_t stream);
 
+/* ---- Rows sorted by expert and back (for expert products of the caller's own: unquantised,
+ * adapted or trained experts between the same router and the same combine), with their gradients.
+ *
+ * Rows are bf16, fp16 or fp32 (MOE_DTYPE_*), H values each, any H >= 1; *_stride is the distance
+ * between rows in elements (inputs: >= 0, 0 repeats one row; outputs: >= H). Rows that start on
+ * 16-byte boundaries with H a multiple of 8 move as 16-byte words, others value by value. Sums are
+ * fp32 in a fixed order (results are bit-identical run to run), rounded once. Outputs must not
+ * overlap inputs unless a comment allows it. T = 0 is a valid empty batch. */
+enum { MOE_DTYPE_BF16 = 0, MOE_DTYPE_F16 = 1, MOE_DTYPE_F32 = 2 };
+
+/* Sorts the T*k pairs by expert and writes each token's row to its pairs' places:
+ *   counts[E], offsets[E+1], perm[T*k], inv[T*k] as moe_permute; xp[inv[t*k+j]] = x[t].
+ * An id outside [0, E) drops its pair (a choice over an expert's capacity): inv = -1, no row. The
+ * kept rows are the first offsets[E]; perm and xp behind them are left as they were. A batch of
+ * at most 2048 pairs is one launch, a larger one two.
+ * Errors: MOE_ERR_ARG, MOE_ERR_SHAPE (E > 256, T*k > 2^31-1). */
+int moe_dispatch(const void* x, int64_t x_stride, int dtype, const int32_t* idx,
+                 int T, int H, int E, int k,
+                 int32_t* counts, int32_t* offsets, int32_t* perm, int32_t* inv,
+                 void* xp, int64_t xp_stride, moe_stream_t stream);
+
+/* Gradient of moe_dispatch: dx[t] = sum_j dxp[inv[t*k+j]], j ascending; dropped pairs (inv outside
+ * [0, T*k)) add nothing, a token with none left gets zeros. */
+int moe_dispatch_backward(const void* dxp, int64_t dxp_stride, int dtype, const int32_t* inv,
+                          int T, int H, int k, void* dx, int64_t dx_stride, moe_stream_t stream);
+
+/* The way back: out[t] = sum_j wts[t*k+j] * yp[inv[t*k+j]], j ascending; dropped pairs add nothing.
+ * yp holds T*k rows. yp_dtype is out_dtype or MOE_DTYPE_F32. */
+int moe_combine(const void* yp, int64_t yp_stride, int yp_dtype, const int32_t* inv, const float* wts,
+                int T, int H, int k, void* out, int64_t out_stride, int out_dtype, moe_stream_t stream);
+
+/* Gradient of moe_combine, one pass over dout and yp:
+ *   dyp[inv[t*k+j]] = wts[t*k+j] * dout[t]   (type of yp; rows no pair points to stay as they were)
+ *   dwts[t*k+j]     = <dout[t], yp[inv[t*k+j]]>   (fp32 [T][k]; 0 for a dropped pair)
+ * dyp or dwts may be NULL (not both); yp may be NULL without dwts. inv comes from moe_dispatch:
+ * no place twice. */
+int moe_combine_backward(const void* dout, int64_t dout_stride, int dout_dtype,
+                         const void* yp, int64_t yp_stride, int yp_dtype,
+                         const int32_t* inv, const float* wts, int T, int H, int k,
+                         void* dyp, int64_t dyp_stride, float* dwts, moe_stream_t stream);
+
+/* Gradient of moe_route_topk's weights towards the logits. The renormalised weights are a softmax
+ * over the k chosen logits, so dlogits[t][idx_j] = w_j * (dwts_j - sum_i w_i * dwts_i), and 0 for
+ * every expert not chosen. idx, wts: the router's outputs [T][k] (an id outside [0, E) is not
+ * written but counts in the sum; an id given twice adds up). dlogits: [T][E], dtype MOE_DTYPE_*.
+ * Errors: MOE_ERR_ARG, MOE_ERR_SHAPE (E > 256). */
+int moe_route_topk_backward(const int32_t* idx, const float* wts, const float* dwts,
+                            int T, int E, int k, void* dlogits, int64_t dlogits_stride, int dtype,
+                            moe_stream_t stream);
+
+/* ---- Norms before and after a block, with its gate and the scaled residual. Types, strides and
+ * sums as above; H <= 16384; every tensor of rows in a call has the same type `dtype`, and so have
+ * the norms' weights [H] and the per-channel gate. rms(v) = v / sqrt(mean(v^2) + eps), eps > 0.
+ *
+ *   before the block:  x      = rms(h) * w
+ *   after the block:   u      = rms(y) * w   with MOE_NORM_Y, else y
+ *                      h_out  = alpha * h + g * u
+ *                      x_next = rms(h_out) * w_next   with MOE_NORM_NEXT (of the fp32 h_out, before
+ *                                                     it is rounded)
+ * A weight may be NULL (ones). The gate g: none (1), one value per channel, one per token, or one
+ * per value. */
+enum {
+  MOE_NORM_Y = 1,
+  MOE_NORM_NEXT = 2,
+  MOE_GATE_NONE = 0,
+  MOE_GATE_CHANNEL = 1, /* [H], type `dtype`; gradient fp32 [H]                     */
+  MOE_GATE_TOKEN = 2,   /* fp32 [T]; gradient fp32 [T]                              */
+  MOE_GATE_FULL = 3     /* [T][H] rows, type `dtype`; gradient of the same form     */
+};
+
+/* Scratch of the two *_backward calls below when they write gradients of weights or of a
+ * per-channel gate (partial sums; no initialisation, nothing kept between calls; not to be shared
+ * by calls that can run at the same time). 256-byte aligned. */
+int moe_norm_workspace_bytes(int T, int H, size_t* bytes);
+
+/* x = rms(h) * w. */
+int moe_norm_pre(const void* h, int64_t h_stride, int dtype, const void* w, float eps, int T, int H,
+                 void* x, int64_t x_stride, moe_stream_t stream);
+
+/* dh = dres + d(rms(h) * w)/dh applied to dx; dw (fp32 [H], may be NULL) = sum_t dx * rms(h).
+ * dres: the residual path's gradient, NULL = none; dh may be dres (same stride). */
+int moe_norm_pre_backward(const void* dx, int64_t dx_stride, const void* h, int64_t h_stride, int dtype,
+                          const void* w, float eps, int T, int H, const void* dres, int64_t dres_stride,
+                          void* dh, int64_t dh_stride, float* dw,
+                          void* workspace, size_t workspace_bytes, moe_stream_t stream);
+
+/* The norm after a block, its gate, the scaled residual and (MOE_NORM_NEXT) the next block's norm in
+ * one pass. h_out may be h (same stride). flags: MOE_NORM_*. */
+int moe_norm_post(const void* y, int64_t y_stride, const void* h, int64_t h_stride, int dtype,
+                  const void* w, const void* gate, int64_t gate_stride, int gate_mode, float alpha, float eps,
+                  int T, int H, int flags, void* h_out, int64_t h_out_stride,
+                  const void* w_next, void* x_next, int64_t x_next_stride, moe_stream_t stream);
+
+/* moe_combine and moe_norm_post in one launch: y[t] = sum_j wts[t*k+j] * yp[inv[t*k+j]] is normed in
+ * fp32, without being rounded in between. yp_dtype is dtype or MOE_DTYPE_F32. y_out (may be NULL)
+ * keeps y (rounded to dtype) for the backward pass. */
+int moe_combine_norm_post(const void* yp, int64_t yp_stride, int yp_dtype, const int32_t* inv,
+                          const float* wts, int k, const void* h, int64_t h_stride, int dtype,
+                          const void* w, const void* gate, int64_t gate_stride, int gate_mode,
+                          float alpha, float eps, int T, int H, int flags,
+                          void* h_out, int64_t h_out_stride,
+                          const void* w_next, void* x_next, int64_t x_next_stride,
+                          void* y_out, int64_t y_out_stride, moe_stream_t stream);
+
+/* Gradient of moe_norm_post in one pass over its inputs. dh_out: gradient of h_out; with
+ * MOE_NORM_NEXT, dx_next: gradient of x_next, and h_out the forward's output. With
+ *   d = dh_out + d(rms(h_out) * w_next)/dh_out applied to dx_next
+ * writes dh = alpha * d, dy = d(u)/dy applied to g * d, and where not NULL dw (fp32 [H]) =
+ * sum_t g * d * rms(y), dw_next (fp32 [H]) = sum_t dx_next * rms(h_out), dgate = d * u (summed over
+ * the tokens for a per-channel gate, over the channels for a per-token one). The statistics are
+ * computed again from y and h_out. dh may be dh_out (same stride). */
+int moe_norm_post_backward(const void* dh_out, int64_t dh_out_stride, const void* y, int64_t y_stride,
+                           int dtype, const void* w, const void* gate, int64_t gate_stride, int gate_mode,
+                           float alpha, float eps, int T, int H, int flags,
+                           const void* h_out, int64_t h_out_stride, const void* w_next,
+                           const void* dx_next, int64_t dx_next_stride,
+                           void* dh, int64_t dh_stride, void* dy, int64_t dy_stride,
+                           float* dw, void* dgate, int64_t dgate_stride, float* dw_next,
+                           void* workspace, size_t workspace_bytes, moe_stream_t stream);
+
 /* ---- GPU slot cache (abstract: "configurable GPU-resident slot cache", experts kept in
  * pinned host memory). One cache per layer: S device slots, each holding one expert's packed
  * W13, W2 and their scales; misses are copied from the pinned host bank with

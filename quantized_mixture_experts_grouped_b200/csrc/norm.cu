@@ -1,0 +1,612 @@
+// Norms before and after a block, fused with the block's gate, the scaled residual and the next
+// block's norm; and their gradients. The block here is the MoE layer of "Every Expert Counts:
+// ExactMoE for Memory-Efficient W4A16 Inference" (Abstract): the residual stream around it stays
+// in 16 bits, every statistic and sum is fp32.
+//
+//   pre   x = rms(h) w                        rms(v) = v r(v),  r(v) = (mean(v^2) + eps)^(-1/2)
+//   post  u = rms(y) w (or y);  h' = alpha h + g u;  x' = rms(h') w'
+//   Gradient of rms(v) w towards v, applied to d, with n = rms(v):  r (w d - n mean(w d n)).
+//
+// All of it moves each row once and does some 10 to 25 flops per value: bound by HBM traffic for
+// large batches, by the latency of one launch for small ones. A block holds one row in registers
+// (8 or 16 values per thread) between its loads and its stores, so no row is read twice.
+#include "rows.cuh"
+
+namespace moe {
+
+namespace {
+
+constexpr int kMaxNormH = 16384;
+constexpr int kSums = 3;             // column sums of the backward pass: dw, dgate, dw_next
+
+struct PostArgs {
+  const void *y, *h, *w, *gate, *w_next;
+  void *h_out, *x_next, *y_out;
+  int64_t ldy, ldh, ldg, ldho, ldx, ldyo;
+  const int32_t* inv;                // fused combine: y = sum_j wts * yp[inv]
+  const float* wts;
+  int k, P, H, gate_mode;
+  bool norm_y, next;
+  float alpha, eps;
+};
+
+// The value of one weight or gate vector at this thread's columns (ones where there is none).
+template <bool VEC, typename T>
+__device__ __forceinline__ void weight8(const void* w, int c, int nt, int tid, int H, float (&f)[8]) {
+  if (w) {
+    load8<VEC>(static_cast<const T*>(w), c, nt, tid, H, f);
+  } else {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) f[e] = 1.f;
+  }
+}
+
+// The gate of token t at this thread's columns.
+template <bool VEC, typename T>
+__device__ __forceinline__ void gate8(const void* g, int mode, int64_t ld, int64_t t, int c, int nt, int tid, int H,
+                                      float (&f)[8]) {
+  if (mode == MOE_GATE_CHANNEL || mode == MOE_GATE_FULL) {
+    load8<VEC>(static_cast<const T*>(g) + (mode == MOE_GATE_FULL ? t * ld : 0), c, nt, tid, H, f);
+  } else {
+    const float v = mode == MOE_GATE_TOKEN ? static_cast<const float*>(g)[t] : 1.f;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) f[e] = v;
+  }
+}
+
+template <typename T, bool VEC, int NC>
+__global__ void __launch_bounds__(1024) norm_pre_kernel(const T* __restrict__ h, int64_t ldh, const T* __restrict__ w,
+                                                        float eps, int H, T* __restrict__ x, int64_t ldx) {
+  __shared__ float buf[32];
+  pdl_begin();
+  const int64_t t = blockIdx.x;
+  const int nt = blockDim.x, tid = threadIdx.x;
+  float v[NC][8], wv[NC][8], ss[1] = {0.f};
+#pragma unroll
+  for (int c = 0; c < NC; ++c) load8<VEC>(h + t * ldh, c, nt, tid, H, v[c]);
+#pragma unroll
+  for (int c = 0; c < NC; ++c) weight8<VEC, T>(w, c, nt, tid, H, wv[c]);
+#pragma unroll
+  for (int c = 0; c < NC; ++c)
+#pragma unroll
+    for (int e = 0; e < 8; ++e) ss[0] = fmaf(v[c][e], v[c][e], ss[0]);
+  block_sums<1>(ss, buf);
+  const float r = rsqrtf(ss[0] / H + eps);
+#pragma unroll
+  for (int c = 0; c < NC; ++c) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[c][e] = v[c][e] * r * wv[c][e];
+    store8<VEC>(x + t * ldx, c, nt, tid, H, v[c]);
+  }
+}
+
+// YT: type of the rows y comes from; FUSED: y is the combine of its token's rows. h_out may be h:
+// a thread reads its values of the row before it writes them, and no other thread reads them.
+template <typename T, typename YT, bool FUSED, bool VEC, int NC>
+__global__ void __launch_bounds__(1024) norm_post_kernel(const PostArgs a) {
+  __shared__ float buf[2][32];
+  pdl_begin();
+  const int64_t t = blockIdx.x;
+  const int nt = blockDim.x, tid = threadIdx.x, H = a.H;
+  float h[NC][8], y[NC][8], s[1] = {0.f};
+  const T* hrow = static_cast<const T*>(a.h) + t * a.ldh;
+#pragma unroll
+  for (int c = 0; c < NC; ++c) load8<VEC>(hrow, c, nt, tid, H, h[c]);
+#pragma unroll
+  for (int c = 0; c < NC; ++c) {
+    if (FUSED) {
+      weighted_rows<VEC>(static_cast<const YT*>(a.y), a.ldy, a.inv + t * a.k, a.wts + t * a.k, a.k, a.P, c, nt, tid, H,
+                         y[c]);
+      if (a.y_out) store8<VEC>(static_cast<T*>(a.y_out) + t * a.ldyo, c, nt, tid, H, y[c]);
+    } else {
+      load8<VEC>(static_cast<const YT*>(a.y) + t * a.ldy, c, nt, tid, H, y[c]);
+    }
+  }
+  if (a.norm_y) {
+#pragma unroll
+    for (int c = 0; c < NC; ++c)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) s[0] = fmaf(y[c][e], y[c][e], s[0]);
+    block_sums<1>(s, buf[0]);
+    const float q = rsqrtf(s[0] / H + a.eps);
+#pragma unroll
+    for (int c = 0; c < NC; ++c) {
+      float w[8];
+      weight8<VEC, T>(a.w, c, nt, tid, H, w);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) y[c][e] = y[c][e] * q * w[e];
+    }
+  }
+  s[0] = 0.f;
+#pragma unroll
+  for (int c = 0; c < NC; ++c) {
+    float g[8];
+    gate8<VEC, T>(a.gate, a.gate_mode, a.ldg, t, c, nt, tid, H, g);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      h[c][e] = fmaf(a.alpha, h[c][e], g[e] * y[c][e]);
+      s[0] = fmaf(h[c][e], h[c][e], s[0]);
+    }
+    store8<VEC>(static_cast<T*>(a.h_out) + t * a.ldho, c, nt, tid, H, h[c]);
+  }
+  if (!a.next) return;
+  block_sums<1>(s, buf[1]);
+  const float r = rsqrtf(s[0] / H + a.eps);
+#pragma unroll
+  for (int c = 0; c < NC; ++c) {
+    float w[8];
+    weight8<VEC, T>(a.w_next, c, nt, tid, H, w);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) h[c][e] = h[c][e] * r * w[e];
+    store8<VEC>(static_cast<T*>(a.x_next) + t * a.ldx, c, nt, tid, H, h[c]);
+  }
+}
+
+struct BackArgs {
+  const void *dho, *y, *ho, *dx, *w, *gate, *w_next;   // dho may be null (no residual gradient)
+  void *dh, *dy, *dgate;
+  float *dw, *dw_next, *part;      // part: fp32 [blocks][kSums][H], used with more than one block
+  int64_t lddho, ldy, ldho, lddx, ldg, lddh, lddy, lddg;
+  int T, H, gate_mode;
+  bool has_y, norm_y, next;        // has_y false: the gradient of the norm before a block
+  float alpha, eps;
+};
+
+// One block takes rows blockIdx.x, + gridDim.x, ...; every thread keeps the same columns, so the
+// sums over the tokens stay in its registers and leave once per block, as partial sums that
+// norm_sums_kernel adds in block order (no atomics: bit-identical run to run).
+template <typename T, bool VEC, int NC, int MAXT>
+__global__ void __launch_bounds__(MAXT) norm_backward_kernel(const BackArgs a) {
+  __shared__ float buf[2][32 * 3];
+  int flip = 0;                    // the buffer of the next block-wide sums: never the one of the last
+  pdl_begin();
+  const int nt = blockDim.x, tid = threadIdx.x, H = a.H;
+  const float inv_h = 1.f / (float)H;
+  float sw[NC][8], sg[NC][8], sn[NC][8];
+#pragma unroll
+  for (int c = 0; c < NC; ++c)
+#pragma unroll
+    for (int e = 0; e < 8; ++e) sw[c][e] = sg[c][e] = sn[c][e] = 0.f;
+  for (int64_t t = blockIdx.x; t < a.T; t += gridDim.x) {
+    float d[NC][8], y[NC][8], h[NC][8], x[NC][8];
+    float s[3] = {0.f, 0.f, 0.f};     // sum h'^2, sum w' dx h', sum y^2
+#pragma unroll
+    for (int c = 0; c < NC; ++c) {
+      if (a.dho) load8<VEC>(static_cast<const T*>(a.dho) + t * a.lddho, c, nt, tid, H, d[c]);
+      if (a.has_y) load8<VEC>(static_cast<const T*>(a.y) + t * a.ldy, c, nt, tid, H, y[c]);
+      if (a.next) {
+        load8<VEC>(static_cast<const T*>(a.ho) + t * a.ldho, c, nt, tid, H, h[c]);
+        load8<VEC>(static_cast<const T*>(a.dx) + t * a.lddx, c, nt, tid, H, x[c]);
+      }
+    }
+#pragma unroll
+    for (int c = 0; c < NC; ++c) {
+      if (!a.dho) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) d[c][e] = 0.f;
+      }
+      if (a.next) {
+        float w[8];
+        weight8<VEC, T>(a.w_next, c, nt, tid, H, w);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          s[0] = fmaf(h[c][e], h[c][e], s[0]);
+          s[1] = fmaf(w[e] * x[c][e], h[c][e], s[1]);
+        }
+      }
+      if (a.norm_y) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) s[2] = fmaf(y[c][e], y[c][e], s[2]);
+      }
+    }
+    if (a.next || a.norm_y) {
+      block_sums<3>(s, buf[flip]);
+      flip ^= 1;
+    }
+    if (a.next) {
+      const float r = rsqrtf(s[0] * inv_h + a.eps);
+      const float m = s[1] * inv_h * r;              // mean(w' dx n), n = h' r
+#pragma unroll
+      for (int c = 0; c < NC; ++c) {
+        float w[8];
+        weight8<VEC, T>(a.w_next, c, nt, tid, H, w);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const float n = h[c][e] * r;
+          d[c][e] += r * (w[e] * x[c][e] - n * m);
+          sn[c][e] = fmaf(x[c][e], n, sn[c][e]);
+        }
+      }
+    }
+    // dh = alpha d
+#pragma unroll
+    for (int c = 0; c < NC; ++c) {
+      float o[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) o[e] = a.alpha * d[c][e];
+      store8<VEC>(static_cast<T*>(a.dh) + t * a.lddh, c, nt, tid, H, o);
+    }
+    if (!a.has_y) continue;
+    const float q = a.norm_y ? rsqrtf(s[2] * inv_h + a.eps) : 1.f;
+    float z[2] = {0.f, 0.f};          // sum w du n, sum d u
+#pragma unroll
+    for (int c = 0; c < NC; ++c) {
+      float w[8], g[8];
+      if (a.norm_y) weight8<VEC, T>(a.w, c, nt, tid, H, w);
+      gate8<VEC, T>(a.gate, a.gate_mode, a.ldg, t, c, nt, tid, H, g);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const float n = y[c][e] * q, we = a.norm_y ? w[e] : 1.f;
+        const float du = g[e] * d[c][e];
+        const float dg = d[c][e] * n * we;           // d u
+        z[1] += dg;
+        if (a.gate_mode == MOE_GATE_CHANNEL) sg[c][e] += dg;
+        if (a.norm_y) sw[c][e] = fmaf(du, n, sw[c][e]);
+        z[0] = fmaf(we * du, n, z[0]);
+        g[e] = dg;
+        d[c][e] = we * du;
+        y[c][e] = n;
+      }
+      if (a.gate_mode == MOE_GATE_FULL && a.dgate)
+        store8<VEC>(static_cast<T*>(a.dgate) + t * a.lddg, c, nt, tid, H, g);
+    }
+    if (a.norm_y || a.gate_mode == MOE_GATE_TOKEN) {
+      block_sums<2>(z, buf[flip]);
+      flip ^= 1;
+    }
+    if (a.gate_mode == MOE_GATE_TOKEN && a.dgate && tid == 0) static_cast<float*>(a.dgate)[t] = z[1];
+    const float m = a.norm_y ? z[0] * inv_h : 0.f;
+#pragma unroll
+    for (int c = 0; c < NC; ++c) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) d[c][e] = a.norm_y ? q * (d[c][e] - y[c][e] * m) : d[c][e];
+      store8<VEC>(static_cast<T*>(a.dy) + t * a.lddy, c, nt, tid, H, d[c]);
+    }
+  }
+  float* out[kSums] = {a.dw, a.gate_mode == MOE_GATE_CHANNEL ? static_cast<float*>(a.dgate) : nullptr, a.dw_next};
+#pragma unroll
+  for (int i = 0; i < kSums; ++i) {
+    if (!out[i]) continue;
+    float* o = gridDim.x == 1 ? out[i] : a.part + ((int64_t)blockIdx.x * kSums + i) * H;
+#pragma unroll
+    for (int c = 0; c < NC; ++c) {
+      const float(&v)[8] = i == 0 ? sw[c] : i == 1 ? sg[c] : sn[c];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const int n = col_of<VEC>(c, e, nt, tid);
+        if (n < H) o[n] = v[e];
+      }
+    }
+  }
+}
+
+// Adds the blocks' partial sums: 32 columns by 32 runs of blocks per block, each run in block
+// order, then the runs in order.
+__global__ void __launch_bounds__(1024) norm_sums_kernel(const float* __restrict__ part, int blocks, int H, float* o0,
+                                                         float* o1, float* o2) {
+  __shared__ float sum[32][33];
+  pdl_begin();
+  float* out = blockIdx.y == 0 ? o0 : blockIdx.y == 1 ? o1 : o2;
+  if (!out) return;
+  const int lane = threadIdx.x & 31, run = threadIdx.x >> 5;
+  const int n = blockIdx.x * 32 + lane, per = (blocks + 31) / 32;
+  float v = 0.f;
+  if (n < H) {
+    const int b1 = min((run + 1) * per, blocks);
+#pragma unroll 4
+    for (int b = run * per; b < b1; ++b) v += part[((int64_t)b * kSums + blockIdx.y) * H + n];
+  }
+  sum[run][lane] = v;
+  __syncthreads();
+  if (run == 0 && n < H) {
+    float total = 0.f;
+#pragma unroll
+    for (int i = 0; i < 32; ++i) total += sum[i][lane];
+    out[n] = total;
+  }
+}
+
+// ---- host side ----
+
+// Threads and chunks per thread for rows of H values.
+struct Shape {
+  int nt, nc;
+};
+Shape shape_of(int H, int most) {
+  const int nt = row_threads(H, most);
+  if (H <= 8 * nt) return {nt, 1};
+  return {row_threads(ceil_div(H, 2), 1024), 2};
+}
+
+// Calls f(typed null pointer) for the row type.
+template <typename F>
+int by_type(int dtype, F f) {
+  if (dtype == MOE_DTYPE_BF16) return f((__nv_bfloat16*)nullptr);
+  if (dtype == MOE_DTYPE_F16) return f((__half*)nullptr);
+  return f((float*)nullptr);
+}
+
+int norm_sms() {
+  int dev = 0, n = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n <= 0) {
+    cudaGetLastError();
+    n = 148;
+  }
+  return n;
+}
+
+// Blocks of the backward kernel never exceed this, so that the workspace's size does not depend on
+// the device.
+constexpr int kMaxBlocks = 592;
+int back_blocks(int T, int nt) {
+  const int per_sm = nt <= 256 ? 2 : 1;
+  const int b = norm_sms() * per_sm;
+  return T < b ? T : b < kMaxBlocks ? b : kMaxBlocks;
+}
+size_t norm_ws(int T, int H) {
+  const size_t b = T < kMaxBlocks ? (T > 0 ? T : 1) : kMaxBlocks;
+  return align_up(b * kSums * (size_t)H * sizeof(float), 256);
+}
+
+int check_norm(const char* me, int T, int H, int dtype, float eps) {
+  if (T < 0 || H < 1) return fail(MOE_ERR_ARG, "%s: bad sizes T=%d H=%d", me, T, H);
+  if (H > kMaxNormH) return fail(MOE_ERR_SHAPE, "%s: H=%d exceeds %d", me, H, kMaxNormH);
+  if (!dtype_size(dtype)) return fail(MOE_ERR_ARG, "%s: unknown type %d", me, dtype);
+  if (!(eps > 0.f) || eps > 1e30f) return fail(MOE_ERR_ARG, "%s: eps must be positive and finite", me);
+  return MOE_OK;
+}
+
+// Rows that are written lie apart; rows only read may repeat (stride 0).
+int check_ld(const char* me, const char* name, const void* p, int64_t ld, int T, int H, bool written) {
+  if (p && (ld < 0 || (written && T > 1 && ld < H)))
+    return fail(MOE_ERR_ARG, "%s: row stride %lld of %s (H=%d)", me, (long long)ld, name, H);
+  return MOE_OK;
+}
+
+int check_gate(const char* me, const void* gate, int mode) {
+  if (mode < MOE_GATE_NONE || mode > MOE_GATE_FULL) return fail(MOE_ERR_ARG, "%s: unknown gate mode %d", me, mode);
+  if ((mode != MOE_GATE_NONE) != (gate != nullptr))
+    return fail(MOE_ERR_ARG, "%s: gate pointer and gate mode %d do not go together", me, mode);
+  return MOE_OK;
+}
+
+bool gate16(const void* gate, int mode, int64_t ld, size_t z) {
+  if (mode == MOE_GATE_CHANNEL) return rows16(gate, 0, z);
+  return mode != MOE_GATE_FULL || rows16(gate, ld, z);
+}
+
+template <typename T, typename YT, bool FUSED>
+int launch_post(const PostArgs& a, int rows, bool vec, cudaStream_t s) {
+  const Shape sh = shape_of(a.H, 1024);
+  auto kern = sh.nc == 1 ? (vec ? norm_post_kernel<T, YT, FUSED, true, 1> : norm_post_kernel<T, YT, FUSED, false, 1>)
+                         : (vec ? norm_post_kernel<T, YT, FUSED, true, 2> : norm_post_kernel<T, YT, FUSED, false, 2>);
+  note_launch();
+  return check_cuda(launch_pdl(kern, dim3(rows), dim3(sh.nt), 0, s, a), "norm_post_kernel");
+}
+
+// Checks common to moe_norm_post and moe_combine_norm_post; *vec receives whether rows move as words.
+int check_post(const char* me, const PostArgs& a, int T, int H, int dtype, int flags, bool* vec) {
+  if (int rc = check_norm(me, T, H, dtype, a.eps)) return rc;
+  if (flags & ~(MOE_NORM_Y | MOE_NORM_NEXT)) return fail(MOE_ERR_ARG, "%s: unknown flags %d", me, flags);
+  if (int rc = check_gate(me, a.gate, a.gate_mode)) return rc;
+  if (T > 0 && (!a.y || !a.h || !a.h_out || (a.next && !a.x_next))) return fail(MOE_ERR_ARG, "%s: null pointer", me);
+  if (T > 0 && ((a.h_out == a.h && a.ldho != a.ldh) || a.h_out == a.y || (a.next && (a.x_next == a.h_out || a.x_next == a.h || a.x_next == a.y))))
+    return fail(MOE_ERR_ARG, "%s: outputs overlap", me);
+  const size_t z = dtype_size(dtype);
+  if (int rc = check_ld(me, "h", a.h, a.ldh, T, H, false)) return rc;
+  if (int rc = check_ld(me, "h_out", a.h_out, a.ldho, T, H, true)) return rc;
+  if (a.next)
+    if (int rc = check_ld(me, "x_next", a.x_next, a.ldx, T, H, true)) return rc;
+  if (a.gate_mode == MOE_GATE_FULL)
+    if (int rc = check_ld(me, "gate", a.gate, a.ldg, T, H, false)) return rc;
+  *vec = H % 8 == 0 && rows16(a.h, a.ldh, z) && rows16(a.h_out, a.ldho, z) && (!a.norm_y || rows16(a.w, 0, z)) &&
+         (!a.next || (rows16(a.w_next, 0, z) && rows16(a.x_next, a.ldx, z))) && gate16(a.gate, a.gate_mode, a.ldg, z);
+  return MOE_OK;
+}
+
+// The kernel built for a block of this size: the fewer threads, the more registers each has.
+template <typename T, bool VEC>
+auto back_kernel(Shape sh) {
+  if (sh.nc == 2) return norm_backward_kernel<T, VEC, 2, 1024>;
+  if (sh.nt <= 256) return norm_backward_kernel<T, VEC, 1, 256>;
+  if (sh.nt <= 512) return norm_backward_kernel<T, VEC, 1, 512>;
+  return norm_backward_kernel<T, VEC, 1, 1024>;
+}
+
+int launch_back(const char* me, BackArgs& a, int dtype, bool vec, void* ws, size_t ws_bytes, cudaStream_t s) {
+  const bool channel = a.gate_mode == MOE_GATE_CHANNEL;
+  float* sums[kSums] = {a.dw, channel ? static_cast<float*>(a.dgate) : nullptr, a.dw_next};
+  const bool any = sums[0] || sums[1] || sums[2];
+  if (a.T == 0) {    // the sums over no tokens
+    for (float* p : sums)
+      if (p)
+        if (int rc = check_cuda(cudaMemsetAsync(p, 0, sizeof(float) * a.H, s), me)) return rc;
+    return MOE_OK;
+  }
+  const Shape sh = shape_of(a.H, 1024);
+  const int blocks = back_blocks(a.T, sh.nt);
+  if (any && blocks > 1) {
+    const size_t need = norm_ws(a.T, a.H);
+    if (!ws || ws_bytes < need)
+      return fail(MOE_ERR_ARG, "%s: workspace of %zu bytes is smaller than the %zu needed", me, ws ? ws_bytes : 0, need);
+    if (reinterpret_cast<uintptr_t>(ws) & 255) return fail(MOE_ERR_ARG, "%s: workspace must be 256-byte aligned", me);
+    a.part = static_cast<float*>(ws);
+  }
+  note_launch();
+  int rc = by_type(dtype, [&](auto* p) {
+    using T = std::remove_pointer_t<decltype(p)>;
+    auto kern = vec ? back_kernel<T, true>(sh) : back_kernel<T, false>(sh);
+    return check_cuda(launch_pdl(kern, dim3(blocks), dim3(sh.nt), 0, s, a), "norm_backward_kernel");
+  });
+  if (rc || !any || blocks == 1) return rc;
+  note_launch();
+  return check_cuda(launch_pdl(norm_sums_kernel, dim3(ceil_div(a.H, 32), kSums), dim3(1024), 0, s,
+                               (const float*)a.part, blocks, a.H, sums[0], sums[1], sums[2]),
+                    "norm_sums_kernel");
+}
+
+}  // namespace
+
+}  // namespace moe
+
+using namespace moe;
+
+MOE_API int moe_norm_workspace_bytes(int T, int H, size_t* bytes) {
+  if (!bytes || T < 0 || H < 1) return fail(MOE_ERR_ARG, "moe_norm_workspace_bytes: bad arguments");
+  if (H > kMaxNormH) return fail(MOE_ERR_SHAPE, "moe_norm_workspace_bytes: H=%d exceeds %d", H, kMaxNormH);
+  *bytes = norm_ws(T, H);
+  return MOE_OK;
+}
+
+MOE_API int moe_norm_pre(const void* h, int64_t h_stride, int dtype, const void* w, float eps, int T, int H, void* x,
+                         int64_t x_stride, moe_stream_t stream) {
+  const char* me = "moe_norm_pre";
+  if (int rc = check_norm(me, T, H, dtype, eps)) return rc;
+  if (T > 0 && (!h || !x)) return fail(MOE_ERR_ARG, "%s: null pointer", me);
+  if (T > 0 && x == h) return fail(MOE_ERR_ARG, "%s: x overlaps h", me);
+  if (int rc = check_ld(me, "h", h, h_stride, T, H, false)) return rc;
+  if (int rc = check_ld(me, "x", x, x_stride, T, H, true)) return rc;
+  if (T == 0) return MOE_OK;
+  const size_t z = dtype_size(dtype);
+  const bool vec = H % 8 == 0 && rows16(h, h_stride, z) && rows16(x, x_stride, z) && rows16(w, 0, z);
+  const Shape sh = shape_of(H, 1024);
+  note_launch();
+  return by_type(dtype, [&](auto* p) {
+    using T_ = std::remove_pointer_t<decltype(p)>;
+    auto kern = sh.nc == 1 ? (vec ? norm_pre_kernel<T_, true, 1> : norm_pre_kernel<T_, false, 1>)
+                           : (vec ? norm_pre_kernel<T_, true, 2> : norm_pre_kernel<T_, false, 2>);
+    return check_cuda(launch_pdl(kern, dim3(T), dim3(sh.nt), 0, reinterpret_cast<cudaStream_t>(stream),
+                                 static_cast<const T_*>(h), h_stride, static_cast<const T_*>(w), eps, H,
+                                 static_cast<T_*>(x), x_stride),
+                      "norm_pre_kernel");
+  });
+}
+
+MOE_API int moe_norm_pre_backward(const void* dx, int64_t dx_stride, const void* h, int64_t h_stride, int dtype,
+                                  const void* w, float eps, int T, int H, const void* dres, int64_t dres_stride,
+                                  void* dh, int64_t dh_stride, float* dw, void* workspace, size_t workspace_bytes,
+                                  moe_stream_t stream) {
+  const char* me = "moe_norm_pre_backward";
+  if (int rc = check_norm(me, T, H, dtype, eps)) return rc;
+  if (T > 0 && (!dx || !h || !dh)) return fail(MOE_ERR_ARG, "%s: null pointer", me);
+  if (T > 0 && (dh == dx || dh == h || (dh == dres && dh_stride != dres_stride)))
+    return fail(MOE_ERR_ARG, "%s: dh overlaps an input", me);
+  if (int rc = check_ld(me, "dx", dx, dx_stride, T, H, false)) return rc;
+  if (int rc = check_ld(me, "h", h, h_stride, T, H, false)) return rc;
+  if (int rc = check_ld(me, "dres", dres, dres_stride, T, H, false)) return rc;
+  if (int rc = check_ld(me, "dh", dh, dh_stride, T, H, true)) return rc;
+  const size_t z = dtype_size(dtype);
+  const bool vec = H % 8 == 0 && rows16(dx, dx_stride, z) && rows16(h, h_stride, z) && rows16(dres, dres_stride, z) &&
+                   rows16(dh, dh_stride, z) && rows16(w, 0, z);
+  BackArgs a{};
+  a.dho = dres; a.lddho = dres_stride; a.ho = h; a.ldho = h_stride; a.dx = dx; a.lddx = dx_stride;
+  a.w_next = w; a.dh = dh; a.lddh = dh_stride; a.dw_next = dw;
+  a.T = T; a.H = H; a.gate_mode = MOE_GATE_NONE; a.next = true; a.alpha = 1.f; a.eps = eps;
+  return launch_back(me, a, dtype, vec, workspace, workspace_bytes, reinterpret_cast<cudaStream_t>(stream));
+}
+
+MOE_API int moe_norm_post(const void* y, int64_t y_stride, const void* h, int64_t h_stride, int dtype, const void* w,
+                          const void* gate, int64_t gate_stride, int gate_mode, float alpha, float eps, int T, int H,
+                          int flags, void* h_out, int64_t h_out_stride, const void* w_next, void* x_next,
+                          int64_t x_next_stride, moe_stream_t stream) {
+  const char* me = "moe_norm_post";
+  PostArgs a{};
+  a.y = y; a.ldy = y_stride; a.h = h; a.ldh = h_stride; a.w = w; a.gate = gate; a.ldg = gate_stride;
+  a.gate_mode = gate_mode; a.alpha = alpha; a.eps = eps; a.H = H;
+  a.norm_y = (flags & MOE_NORM_Y) != 0; a.next = (flags & MOE_NORM_NEXT) != 0;
+  a.h_out = h_out; a.ldho = h_out_stride; a.w_next = w_next; a.x_next = x_next; a.ldx = x_next_stride;
+  bool vec = false;
+  if (int rc = check_post(me, a, T, H, dtype, flags, &vec)) return rc;
+  if (int rc = check_ld(me, "y", y, y_stride, T, H, false)) return rc;
+  if (T == 0) return MOE_OK;
+  vec = vec && rows16(y, y_stride, dtype_size(dtype));
+  return by_type(dtype, [&](auto* p) {
+    using T_ = std::remove_pointer_t<decltype(p)>;
+    return launch_post<T_, T_, false>(a, T, vec, reinterpret_cast<cudaStream_t>(stream));
+  });
+}
+
+MOE_API int moe_combine_norm_post(const void* yp, int64_t yp_stride, int yp_dtype, const int32_t* inv,
+                                  const float* wts, int k, const void* h, int64_t h_stride, int dtype, const void* w,
+                                  const void* gate, int64_t gate_stride, int gate_mode, float alpha, float eps, int T,
+                                  int H, int flags, void* h_out, int64_t h_out_stride, const void* w_next,
+                                  void* x_next, int64_t x_next_stride, void* y_out, int64_t y_out_stride,
+                                  moe_stream_t stream) {
+  const char* me = "moe_combine_norm_post";
+  PostArgs a{};
+  a.y = yp; a.ldy = yp_stride; a.h = h; a.ldh = h_stride; a.w = w; a.gate = gate; a.ldg = gate_stride;
+  a.gate_mode = gate_mode; a.alpha = alpha; a.eps = eps; a.H = H;
+  a.norm_y = (flags & MOE_NORM_Y) != 0; a.next = (flags & MOE_NORM_NEXT) != 0;
+  a.h_out = h_out; a.ldho = h_out_stride; a.w_next = w_next; a.x_next = x_next; a.ldx = x_next_stride;
+  a.y_out = y_out; a.ldyo = y_out_stride; a.inv = inv; a.wts = wts; a.k = k;
+  if (k < 1) return fail(MOE_ERR_ARG, "%s: k=%d", me, k);
+  bool vec = false;
+  if (int rc = check_post(me, a, T, H, dtype, flags, &vec)) return rc;
+  if ((int64_t)T * k > INT32_MAX) return fail(MOE_ERR_SHAPE, "%s: T*k exceeds 2^31-1", me);
+  a.P = T * k;
+  if (!dtype_size(yp_dtype) || (yp_dtype != dtype && yp_dtype != MOE_DTYPE_F32))
+    return fail(MOE_ERR_ARG, "%s: rows of type %d with results of type %d", me, yp_dtype, dtype);
+  if (T > 0 && (!inv || !wts)) return fail(MOE_ERR_ARG, "%s: null pointer", me);
+  if (y_out && (y_out == yp || y_out == h || y_out == h_out || y_out == x_next))
+    return fail(MOE_ERR_ARG, "%s: outputs overlap", me);
+  if (int rc = check_ld(me, "yp", yp, yp_stride, T, H, false)) return rc;
+  if (int rc = check_ld(me, "y_out", y_out, y_out_stride, T, H, true)) return rc;
+  if (T == 0) return MOE_OK;
+  vec = vec && rows16(yp, yp_stride, dtype_size(yp_dtype)) && rows16(y_out, y_out_stride, dtype_size(dtype));
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  return by_type(dtype, [&](auto* p) {
+    using T_ = std::remove_pointer_t<decltype(p)>;
+    return yp_dtype == dtype ? launch_post<T_, T_, true>(a, T, vec, s) : launch_post<T_, float, true>(a, T, vec, s);
+  });
+}
+
+MOE_API int moe_norm_post_backward(const void* dh_out, int64_t dh_out_stride, const void* y, int64_t y_stride,
+                                   int dtype, const void* w, const void* gate, int64_t gate_stride, int gate_mode,
+                                   float alpha, float eps, int T, int H, int flags, const void* h_out,
+                                   int64_t h_out_stride, const void* w_next, const void* dx_next,
+                                   int64_t dx_next_stride, void* dh, int64_t dh_stride, void* dy, int64_t dy_stride,
+                                   float* dw, void* dgate, int64_t dgate_stride, float* dw_next, void* workspace,
+                                   size_t workspace_bytes, moe_stream_t stream) {
+  const char* me = "moe_norm_post_backward";
+  if (int rc = check_norm(me, T, H, dtype, eps)) return rc;
+  if (flags & ~(MOE_NORM_Y | MOE_NORM_NEXT)) return fail(MOE_ERR_ARG, "%s: unknown flags %d", me, flags);
+  if (int rc = check_gate(me, gate, gate_mode)) return rc;
+  const bool norm_y = flags & MOE_NORM_Y, next = flags & MOE_NORM_NEXT;
+  if (T > 0 && (!dh_out || !y || !dh || !dy || (next && (!h_out || !dx_next))))
+    return fail(MOE_ERR_ARG, "%s: null pointer", me);
+  if ((dw && !norm_y) || (dw_next && !next) || (dgate && gate_mode == MOE_GATE_NONE))
+    return fail(MOE_ERR_ARG, "%s: gradient asked of something that the call does not have", me);
+  const bool full = gate_mode == MOE_GATE_FULL;
+  if (T > 0 && ((dh == dh_out && dh_stride != dh_out_stride) || dh == y || dh == dy || dy == dh_out || dy == y ||
+                (next && (dh == h_out || dh == dx_next || dy == h_out || dy == dx_next)) ||
+                (full && (dh == gate || dy == gate)) ||
+                (full && dgate && (dgate == dh || dgate == dy || dgate == gate || dgate == y || dgate == dh_out ||
+                                   (next && (dgate == h_out || dgate == dx_next))))))
+    return fail(MOE_ERR_ARG, "%s: an output overlaps another tensor", me);
+  if (int rc = check_ld(me, "dh_out", dh_out, dh_out_stride, T, H, false)) return rc;
+  if (int rc = check_ld(me, "y", y, y_stride, T, H, false)) return rc;
+  if (int rc = check_ld(me, "dh", dh, dh_stride, T, H, true)) return rc;
+  if (int rc = check_ld(me, "dy", dy, dy_stride, T, H, true)) return rc;
+  if (next) {
+    if (int rc = check_ld(me, "h_out", h_out, h_out_stride, T, H, false)) return rc;
+    if (int rc = check_ld(me, "dx_next", dx_next, dx_next_stride, T, H, false)) return rc;
+  }
+  if (full) {
+    if (int rc = check_ld(me, "gate", gate, gate_stride, T, H, false)) return rc;
+    if (int rc = check_ld(me, "dgate", dgate, dgate_stride, T, H, true)) return rc;
+  }
+  const size_t z = dtype_size(dtype);
+  const bool vec = H % 8 == 0 && rows16(dh_out, dh_out_stride, z) && rows16(y, y_stride, z) &&
+                   rows16(dh, dh_stride, z) && rows16(dy, dy_stride, z) && (!norm_y || rows16(w, 0, z)) &&
+                   (!next || (rows16(h_out, h_out_stride, z) && rows16(dx_next, dx_next_stride, z) &&
+                              rows16(w_next, 0, z))) &&
+                   gate16(gate, gate_mode, gate_stride, z) && (!full || rows16(dgate, dgate_stride, z));
+  BackArgs a{};
+  a.dho = dh_out; a.lddho = dh_out_stride; a.y = y; a.ldy = y_stride; a.ho = h_out; a.ldho = h_out_stride;
+  a.dx = dx_next; a.lddx = dx_next_stride; a.w = w; a.gate = gate; a.ldg = gate_stride; a.w_next = w_next;
+  a.dh = dh; a.lddh = dh_stride; a.dy = dy; a.lddy = dy_stride; a.dgate = dgate; a.lddg = dgate_stride;
+  a.dw = dw; a.dw_next = dw_next; a.T = T; a.H = H; a.gate_mode = gate_mode;
+  a.has_y = true; a.norm_y = norm_y; a.next = next; a.alpha = alpha; a.eps = eps;
+  return launch_back(me, a, dtype, vec, workspace, workspace_bytes, reinterpret_cast<cudaStream_t>(stream));
+}

@@ -1,0 +1,527 @@
+// Token rows sorted by expert and back, with the router's weights, and their gradients (the steps
+// around the experts' products of "Every Expert Counts: ExactMoE for Memory-Efficient W4A16
+// Inference", Abstract: all selected experts run through fused grouped kernels).
+//
+//   sort      pair p = t*k+j of expert e goes to place offsets[e] + #{p' < p : e' = e}
+//   dispatch  xp[place] = x[t]                    gradient: dx[t] = sum_j dxp[inv[t][j]]
+//   combine   out[t] = sum_j w[t][j] yp[inv[t][j]]
+//             gradient: dyp[inv[t][j]] = w[t][j] dout[t],  dw[t][j] = <dout[t], yp[inv[t][j]]>
+//   router    w = softmax over the k chosen logits, so dlogit[idx_j] = w_j (dw_j - sum_i w_i dw_i)
+//
+// All of it is bound by HBM traffic (large batches) or by the latency of a launch (small ones), so
+// every row is read once and written once, and each operator is one launch, the sort of a large
+// batch one more. Sums are fp32 in a fixed order; each result is rounded once, to its own type.
+#include <cooperative_groups.h>
+
+#include "rows.cuh"
+
+namespace moe {
+
+namespace {
+
+namespace cg = cooperative_groups;
+
+// ------------------------------------------------------------------------------------- sort
+
+constexpr int kSortThreads = 1024;
+constexpr int kSortCluster = 8;
+
+// Stable counting sort of the P pairs by expert in ONE launch: a cluster of blocks, each with a
+// contiguous run of pairs, each warp with a contiguous part of the block's run. A warp counts its
+// pairs per expert (warp match, so equal ids cost one add), the block prefixes its warps' counts,
+// the cluster exchanges the blocks' counts through distributed shared memory, and the warps walk
+// their pairs once more to place them. Integer counts: the result does not depend on timing.
+__global__ void __launch_bounds__(kSortThreads) sort_pairs_kernel(const int32_t* __restrict__ idx, int P, int E,
+                                                                  int32_t* __restrict__ counts,
+                                                                  int32_t* __restrict__ offsets,
+                                                                  int32_t* __restrict__ perm,
+                                                                  int32_t* __restrict__ inv) {
+  __shared__ int32_t wcount[kSortThreads / 32][kMaxExperts];
+  __shared__ int32_t total[kMaxExperts];
+  __shared__ int32_t first[kMaxExperts];
+  __shared__ int32_t wsum[kMaxExperts / 32];
+  cg::cluster_group cluster = cg::this_cluster();
+  const int rank = cluster.block_rank(), nblk = cluster.num_blocks();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, nw = blockDim.x >> 5;
+  const int per_block = (int)(((int64_t)P + nblk - 1) / nblk);
+  const int per_warp = (per_block + 32 * nw - 1) / (32 * nw) * 32;
+  const int64_t b0 = (int64_t)rank * per_block, b1 = min(b0 + per_block, (int64_t)P);
+  const int64_t w0 = b0 + (int64_t)warp * per_warp, w1 = min(w0 + per_warp, b1);
+  for (int e = lane; e < E; e += 32) wcount[warp][e] = 0;
+  pdl_begin();
+  __syncwarp();
+  for (int64_t p0 = w0; p0 < w1; p0 += 32) {
+    int e = p0 + lane < w1 ? idx[p0 + lane] : -1;
+    if ((unsigned)e >= (unsigned)E) e = -1;
+    const unsigned same = __match_any_sync(0xffffffffu, e);
+    if (e >= 0 && (same & ((1u << lane) - 1u)) == 0) wcount[warp][e] += __popc(same);
+    __syncwarp();
+  }
+  __syncthreads();
+  for (int e = threadIdx.x; e < E; e += blockDim.x) {
+    int run = 0;
+    for (int w = 0; w < nw; ++w) {
+      const int c = wcount[w][e];
+      wcount[w][e] = run;
+      run += c;
+    }
+    total[e] = run;
+  }
+  cluster.sync();
+  // each block: pairs of expert e in the blocks before it, and in all of them
+  int all = 0, before = 0;
+  const int e0 = threadIdx.x;
+  if (e0 < E) {
+    for (int r = 0; r < nblk; ++r) {
+      const int c = *cluster.map_shared_rank(&total[e0], r);
+      if (r < rank) before += c;
+      all += c;
+    }
+  }
+  // exclusive prefix over the experts: within a warp, then over the (at most 8) warps that hold one
+  int incl = all;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int v = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += v;
+  }
+  if (e0 < kMaxExperts && lane == 31) wsum[warp] = incl;
+  __syncthreads();
+  if (e0 < E) {
+    for (int w = 0; w < warp; ++w) incl += wsum[w];
+    first[e0] = incl - all + before;
+    if (rank == 0) {
+      counts[e0] = all;
+      offsets[e0] = incl - all;
+      if (e0 == E - 1) offsets[E] = incl;
+    }
+  }
+  cluster.sync();   // also: no block leaves while another reads its counts
+  for (int64_t p0 = w0; p0 < w1; p0 += 32) {
+    const int64_t p = p0 + lane;
+    int e = p < w1 ? idx[p] : -1;
+    if ((unsigned)e >= (unsigned)E) e = -1;
+    const unsigned same = __match_any_sync(0xffffffffu, e);
+    const int lower = __popc(same & ((1u << lane) - 1u));
+    int place = -1;
+    if (e >= 0) place = first[e] + wcount[warp][e] + lower;
+    __syncwarp();
+    if (e >= 0 && lower == 0) wcount[warp][e] += __popc(same);
+    __syncwarp();
+    if (p < w1) inv[p] = place;
+    if (place >= 0) perm[place] = (int32_t)p;
+  }
+}
+
+// ------------------------------------------------------------------------------------- dispatch
+
+constexpr int kRowThreads = 256;
+constexpr int kSmallPairs = 2048;
+
+// One token's row to its choices' places; U is the unit moved (16 bytes where the rows allow it).
+template <typename U>
+__device__ __forceinline__ void copy_row(const U* __restrict__ src, U* xp, int64_t ldp, const int32_t* place, int k,
+                                         int n) {
+  for (int i = threadIdx.x; i < n; i += blockDim.x) {
+    const U v = src[i];
+    for (int j = 0; j < k; ++j) {
+      const int p = place[j];
+      if (p >= 0) xp[(int64_t)p * ldp + i] = v;
+    }
+  }
+}
+
+template <typename U>
+__global__ void __launch_bounds__(kRowThreads) copy_rows_kernel(const U* __restrict__ x, int64_t ldx,
+                                                                const int32_t* __restrict__ inv, int k, int n, U* xp,
+                                                                int64_t ldp) {
+  pdl_begin();
+  const int64_t t = blockIdx.x;
+  copy_row(x + t * ldx, xp, ldp, inv + t * k, k, n);
+}
+
+// Sort and copy in one launch for few pairs: block t finds its own k places by counting the pairs
+// that go before each of them (every block reads all P ids; P * k comparisons per block), then
+// copies its row. One more block writes the counts and offsets.
+template <typename U>
+__global__ void __launch_bounds__(kRowThreads) dispatch_small_kernel(const U* __restrict__ x, int64_t ldx,
+                                                                     const int32_t* __restrict__ idx, int T, int E,
+                                                                     int k, int n, int32_t* __restrict__ counts,
+                                                                     int32_t* __restrict__ offsets,
+                                                                     int32_t* __restrict__ perm,
+                                                                     int32_t* __restrict__ inv, U* xp, int64_t ldp) {
+  __shared__ int32_t es[kSmallPairs];
+  __shared__ int32_t place[kSmallPairs];
+  __shared__ int32_t wsum[kMaxExperts / 32];
+  const int P = T * k, t = blockIdx.x;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, nw = blockDim.x >> 5;
+  pdl_begin();
+  for (int p = threadIdx.x; p < P; p += blockDim.x) {
+    const int e = idx[p];
+    es[p] = (unsigned)e < (unsigned)E ? e : INT32_MAX;
+  }
+  if (t == T) {
+    for (int e = threadIdx.x; e < kMaxExperts; e += blockDim.x) place[e] = 0;
+    __syncthreads();
+    for (int p = threadIdx.x; p < P; p += blockDim.x)
+      if (es[p] < E) atomicAdd(&place[es[p]], 1);
+    __syncthreads();
+    const int e = threadIdx.x;   // 256 threads, at most 256 experts
+    const int c = place[e];
+    int incl = c;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int v = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += v;
+    }
+    if (lane == 31) wsum[warp] = incl;
+    __syncthreads();
+    for (int w = 0; w < warp; ++w) incl += wsum[w];
+    if (e < E) {
+      counts[e] = c;
+      offsets[e] = incl - c;
+      if (e == E - 1) offsets[E] = incl;
+    }
+    return;
+  }
+  __syncthreads();
+  for (int j = warp; j < k; j += nw) {
+    const int mine = t * k + j, e = es[mine];
+    int lower = 0;
+    for (int p = lane; p < P; p += 32) lower += es[p] < e || (es[p] == e && p < mine);
+    lower = __reduce_add_sync(0xffffffffu, lower);
+    if (lane == 0) {
+      place[j] = e < E ? lower : -1;
+      inv[mine] = place[j];
+      if (e < E) perm[lower] = mine;
+    }
+  }
+  __syncthreads();
+  copy_row(x + (int64_t)t * ldx, xp, ldp, place, k, n);
+}
+
+template <typename U>
+int dispatch_units(const void* x, int64_t ldx, const int32_t* idx, int T, int E, int k, int n, int32_t* counts,
+                   int32_t* offsets, int32_t* perm, int32_t* inv, void* xp, int64_t ldp, cudaStream_t s) {
+  const U* xs = static_cast<const U*>(x);
+  U* xd = static_cast<U*>(xp);
+  const int64_t P = (int64_t)T * k;
+  if (T > 0 && P <= kSmallPairs) {
+    note_launch();
+    return check_cuda(launch_pdl(dispatch_small_kernel<U>, dim3(T + 1), dim3(kRowThreads), 0, s, xs, ldx, idx, T, E, k,
+                                 n, counts, offsets, perm, inv, xd, ldp),
+                      "dispatch_small_kernel");
+  }
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(kSortCluster);
+  cfg.blockDim = dim3(kSortThreads);
+  cfg.stream = s;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = kSortCluster;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  note_launch();
+  if (int rc = check_cuda(cudaLaunchKernelEx(&cfg, sort_pairs_kernel, idx, (int)P, E, counts, offsets, perm, inv),
+                          "sort_pairs_kernel"))
+    return rc;
+  if (T == 0) return MOE_OK;
+  note_launch();
+  return check_cuda(launch_pdl(copy_rows_kernel<U>, dim3(T), dim3(kRowThreads), 0, s, xs, ldx, (const int32_t*)inv, k,
+                               n, xd, ldp),
+                    "copy_rows_kernel");
+}
+
+// ------------------------------------------------------------------------------------- combine
+
+template <typename YT, typename OT, bool VEC>
+__global__ void __launch_bounds__(kRowThreads) combine_rows_kernel(const YT* __restrict__ yp, int64_t ldy,
+                                                                   const int32_t* __restrict__ inv,
+                                                                   const float* __restrict__ wts, int k, int P, int H,
+                                                                   OT* __restrict__ out, int64_t ldo) {
+  pdl_begin();
+  const int64_t t = blockIdx.x;
+  float v[8];
+  weighted_rows<VEC>(yp, ldy, inv + t * k, wts ? wts + t * k : nullptr, k, P, blockIdx.y, blockDim.x, threadIdx.x, H,
+                     v);
+  store8<VEC>(out + t * ldo, blockIdx.y, blockDim.x, threadIdx.x, H, v);
+}
+
+// Gradient of combine: one block per token. dout's row stays in registers while the token's rows
+// pass by: each is read once (its dot product with dout) and its gradient row written once. The
+// dot products of up to kDots choices are reduced together at the end of the row.
+constexpr int kDots = 8;
+
+template <typename YT, typename OT, bool VEC>
+__global__ void __launch_bounds__(kRowThreads) combine_backward_kernel(const OT* __restrict__ dout, int64_t ldo,
+                                                                       const YT* __restrict__ yp, int64_t ldy,
+                                                                       const int32_t* __restrict__ inv,
+                                                                       const float* __restrict__ wts, int k, int P,
+                                                                       int H, YT* __restrict__ dyp, int64_t lddy,
+                                                                       float* __restrict__ dwts) {
+  __shared__ float buf[2][32 * kDots];
+  pdl_begin();
+  const int64_t t = blockIdx.x;
+  const int nt = blockDim.x, tid = threadIdx.x;
+  const int chunks = (H + 8 * nt - 1) / (8 * nt);
+  const int32_t* it = inv + t * k;
+  const float* wt = wts + t * k;
+  int flip = 0;
+  for (int j0 = 0; j0 < k; j0 += kDots, flip ^= 1) {
+    float dot[kDots], w[kDots];
+    int pos[kDots];
+#pragma unroll
+    for (int b = 0; b < kDots; ++b) {
+      dot[b] = 0.f;
+      const int p = j0 + b < k ? it[j0 + b] : -1;
+      pos[b] = (unsigned)p < (unsigned)P ? p : -1;
+      w[b] = pos[b] >= 0 ? wt[j0 + b] : 0.f;
+    }
+    for (int c = 0; c < chunks; ++c) {
+      float d[8];
+      load8<VEC>(dout + t * ldo, c, nt, tid, H, d);
+      constexpr int B = sizeof(YT) == 2 ? 8 : 4;
+#pragma unroll
+      for (int b0 = 0; b0 < kDots; b0 += B) {
+        Raw8<YT> r[B];
+        if (dwts) {
+#pragma unroll
+          for (int b = 0; b < B; ++b)
+            if (pos[b0 + b] >= 0) r[b] = load_raw<VEC>(yp + (int64_t)pos[b0 + b] * ldy, c, nt, tid, H);
+        }
+#pragma unroll
+        for (int b = 0; b < B; ++b) {
+          if (pos[b0 + b] < 0) continue;
+          if (dyp) {
+            float g[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) g[e] = w[b0 + b] * d[e];
+            store8<VEC>(dyp + (int64_t)pos[b0 + b] * lddy, c, nt, tid, H, g);
+          }
+          if (dwts) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) dot[b0 + b] = fmaf(d[e], RowType<YT>::to(r[b].v[e]), dot[b0 + b]);
+          }
+        }
+      }
+    }
+    if (dwts) {
+      block_sums<kDots>(dot, buf[flip]);
+#pragma unroll
+      for (int b = 0; b < kDots; ++b)
+        if (tid == b && j0 + b < k) dwts[t * k + j0 + b] = pos[b] >= 0 ? dot[b] : 0.f;
+    }
+  }
+}
+
+// ------------------------------------------------------------------------------------- router
+
+constexpr int kRouterWarps = 8;
+
+// One warp per token: lane j holds choice j. The row of E gradients is put together in shared
+// memory (zeros, then the chosen ones; a repeated id adds up in choice order) and written whole.
+template <typename LT>
+__global__ void __launch_bounds__(32 * kRouterWarps) route_backward_kernel(const int32_t* __restrict__ idx,
+                                                                           const float* __restrict__ wts,
+                                                                           const float* __restrict__ dwts, int T,
+                                                                           int E, int k, LT* __restrict__ dlogits,
+                                                                           int64_t ldl) {
+  __shared__ float rows[kRouterWarps][kMaxExperts];
+  pdl_begin();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int64_t t = (int64_t)blockIdx.x * kRouterWarps + warp;
+  if (t >= T) return;
+  float* row = rows[warp];
+  const int32_t* it = idx + t * k;
+  const float *wt = wts + t * k, *dt = dwts + t * k;
+  float mean = 0.f;
+  for (int j = lane; j < k; j += 32) mean = fmaf(wt[j], dt[j], mean);
+  for (int e = lane; e < E; e += 32) row[e] = 0.f;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) mean += __shfl_xor_sync(0xffffffffu, mean, o);
+  __syncwarp();
+  for (int j0 = 0; j0 < k; j0 += 32) {
+    const int j = j0 + lane;
+    int e = j < k ? it[j] : -1;
+    if ((unsigned)e >= (unsigned)E) e = -1;
+    const float g = e >= 0 ? wt[j] * (dt[j] - mean) : 0.f;
+    const unsigned same = __match_any_sync(0xffffffffu, e);
+    const unsigned below = same & ((1u << lane) - 1u);
+    const int turn = e >= 0 ? __popc(below) : 0;
+    const int turns = __reduce_max_sync(0xffffffffu, turn);
+    for (int i = 0; i <= turns; ++i) {
+      if (e >= 0 && turn == i) row[e] += g;
+      __syncwarp();
+    }
+  }
+  LT* out = dlogits + t * ldl;
+  for (int e = lane; e < E; e += 32) out[e] = RowType<LT>::from(row[e]);
+}
+
+// ---- host side ----
+
+// Calls f(typed null pointer, typed null pointer) for the (rows, out) types that are built: equal
+// types, or fp32 rows with 16-bit results.
+template <typename F>
+int by_types(int y, int o, F f) {
+  using B = __nv_bfloat16;
+  using Hf = __half;
+  if (y == MOE_DTYPE_BF16 && o == MOE_DTYPE_BF16) return f((B*)nullptr, (B*)nullptr);
+  if (y == MOE_DTYPE_F16 && o == MOE_DTYPE_F16) return f((Hf*)nullptr, (Hf*)nullptr);
+  if (y == MOE_DTYPE_F32 && o == MOE_DTYPE_F32) return f((float*)nullptr, (float*)nullptr);
+  if (y == MOE_DTYPE_F32 && o == MOE_DTYPE_BF16) return f((float*)nullptr, (B*)nullptr);
+  if (y == MOE_DTYPE_F32 && o == MOE_DTYPE_F16) return f((float*)nullptr, (Hf*)nullptr);
+  return fail(MOE_ERR_ARG, "unsupported types: rows %d with results %d", y, o);
+}
+
+int launch_combine_rows(const void* yp, int64_t ldy, int ydt, const int32_t* inv, const float* wts, int T, int H, int k,
+                        void* out, int64_t ldo, int odt, cudaStream_t s) {
+  if (T == 0) return MOE_OK;
+  const bool vec = H % 8 == 0 && rows16(yp, ldy, dtype_size(ydt)) && rows16(out, ldo, dtype_size(odt));
+  const int nt = row_threads(H, kRowThreads);
+  const dim3 grid(T, ceil_div(H, 8 * nt));
+  note_launch();
+  return by_types(ydt, odt, [&](auto* y, auto* o) {
+    using YT = std::remove_pointer_t<decltype(y)>;
+    using OT = std::remove_pointer_t<decltype(o)>;
+    auto kern = vec ? combine_rows_kernel<YT, OT, true> : combine_rows_kernel<YT, OT, false>;
+    return check_cuda(launch_pdl(kern, grid, dim3(nt), 0, s, static_cast<const YT*>(yp), ldy, inv, wts, k, T * k, H,
+                                 static_cast<OT*>(out), ldo),
+                      "combine_rows_kernel");
+  });
+}
+
+int check_rows(const char* what, int T, int H, int k) {
+  if (T < 0 || H < 1 || k < 1) return fail(MOE_ERR_ARG, "%s: bad sizes T=%d H=%d k=%d", what, T, H, k);
+  if ((int64_t)T * k > INT32_MAX) return fail(MOE_ERR_SHAPE, "%s: T*k exceeds 2^31-1", what);
+  return MOE_OK;
+}
+
+// Strides count elements. Rows that are written lie apart; rows only read may repeat (stride 0).
+int check_stride(const char* what, const char* name, int64_t stride, int64_t rows, int H, bool written) {
+  if (stride < 0 || (written && rows > 1 && stride < H))
+    return fail(MOE_ERR_ARG, "%s: row stride %lld of %s (H=%d)", what, (long long)stride, name, H);
+  return MOE_OK;
+}
+
+int check_dtype(const char* what, int dtype) {
+  return dtype_size(dtype) ? MOE_OK : fail(MOE_ERR_ARG, "%s: unknown type %d", what, dtype);
+}
+
+}  // namespace
+
+int launch_dispatch(const void* x, int64_t ldx, size_t size, const int32_t* idx, int T, int H, int E, int k,
+                    int32_t* counts, int32_t* offsets, int32_t* perm, int32_t* inv, void* xp, int64_t ldp,
+                    cudaStream_t s) {
+  if (H * size % 16 == 0 && rows16(x, ldx, size) && rows16(xp, ldp, size)) {
+    const int per = 16 / (int)size;
+    return dispatch_units<uint4>(x, ldx / per, idx, T, E, k, H / per, counts, offsets, perm, inv, xp, ldp / per, s);
+  }
+  if (size == 4) return dispatch_units<uint32_t>(x, ldx, idx, T, E, k, H, counts, offsets, perm, inv, xp, ldp, s);
+  return dispatch_units<uint16_t>(x, ldx, idx, T, E, k, H, counts, offsets, perm, inv, xp, ldp, s);
+}
+
+}  // namespace moe
+
+using namespace moe;
+
+MOE_API int moe_dispatch(const void* x, int64_t x_stride, int dtype, const int32_t* idx, int T, int H, int E, int k,
+                         int32_t* counts, int32_t* offsets, int32_t* perm, int32_t* inv, void* xp, int64_t xp_stride,
+                         moe_stream_t stream) {
+  const char* me = "moe_dispatch";
+  if (int rc = check_rows(me, T, H, k)) return rc;
+  if (int rc = check_dtype(me, dtype)) return rc;
+  if (E < 1) return fail(MOE_ERR_ARG, "%s: E=%d", me, E);
+  if (E > kMaxExperts) return fail(MOE_ERR_SHAPE, "%s: E=%d exceeds %d", me, E, kMaxExperts);
+  if (!counts || !offsets || (T > 0 && (!x || !idx || !perm || !inv || !xp)))
+    return fail(MOE_ERR_ARG, "%s: null pointer", me);
+  if (T > 0 && x == xp) return fail(MOE_ERR_ARG, "%s: xp overlaps x", me);
+  if (int rc = check_stride(me, "x", x_stride, T, H, false)) return rc;
+  if (int rc = check_stride(me, "xp", xp_stride, (int64_t)T * k, H, true)) return rc;
+  return launch_dispatch(x, x_stride, dtype_size(dtype), idx, T, H, E, k, counts, offsets, perm, inv, xp, xp_stride,
+                         reinterpret_cast<cudaStream_t>(stream));
+}
+
+MOE_API int moe_dispatch_backward(const void* dxp, int64_t dxp_stride, int dtype, const int32_t* inv, int T, int H,
+                                  int k, void* dx, int64_t dx_stride, moe_stream_t stream) {
+  const char* me = "moe_dispatch_backward";
+  if (int rc = check_rows(me, T, H, k)) return rc;
+  if (int rc = check_dtype(me, dtype)) return rc;
+  if (T > 0 && (!dxp || !inv || !dx)) return fail(MOE_ERR_ARG, "%s: null pointer", me);
+  if (T > 0 && dx == dxp) return fail(MOE_ERR_ARG, "%s: dx overlaps dxp", me);
+  if (int rc = check_stride(me, "dxp", dxp_stride, (int64_t)T * k, H, false)) return rc;
+  if (int rc = check_stride(me, "dx", dx_stride, T, H, true)) return rc;
+  return launch_combine_rows(dxp, dxp_stride, dtype, inv, nullptr, T, H, k, dx, dx_stride, dtype,
+                             reinterpret_cast<cudaStream_t>(stream));
+}
+
+MOE_API int moe_combine(const void* yp, int64_t yp_stride, int yp_dtype, const int32_t* inv, const float* wts, int T,
+                        int H, int k, void* out, int64_t out_stride, int out_dtype, moe_stream_t stream) {
+  const char* me = "moe_combine";
+  if (int rc = check_rows(me, T, H, k)) return rc;
+  if (int rc = check_dtype(me, yp_dtype)) return rc;
+  if (int rc = check_dtype(me, out_dtype)) return rc;
+  if (yp_dtype != out_dtype && yp_dtype != MOE_DTYPE_F32)
+    return fail(MOE_ERR_ARG, "%s: rows of type %d with results of type %d", me, yp_dtype, out_dtype);
+  if (T > 0 && (!yp || !inv || !wts || !out)) return fail(MOE_ERR_ARG, "%s: null pointer", me);
+  if (T > 0 && out == yp) return fail(MOE_ERR_ARG, "%s: out overlaps yp", me);
+  if (int rc = check_stride(me, "yp", yp_stride, (int64_t)T * k, H, false)) return rc;
+  if (int rc = check_stride(me, "out", out_stride, T, H, true)) return rc;
+  return launch_combine_rows(yp, yp_stride, yp_dtype, inv, wts, T, H, k, out, out_stride, out_dtype,
+                             reinterpret_cast<cudaStream_t>(stream));
+}
+
+MOE_API int moe_combine_backward(const void* dout, int64_t dout_stride, int dout_dtype, const void* yp,
+                                 int64_t yp_stride, int yp_dtype, const int32_t* inv, const float* wts, int T, int H,
+                                 int k, void* dyp, int64_t dyp_stride, float* dwts, moe_stream_t stream) {
+  const char* me = "moe_combine_backward";
+  if (int rc = check_rows(me, T, H, k)) return rc;
+  if (int rc = check_dtype(me, yp_dtype)) return rc;
+  if (int rc = check_dtype(me, dout_dtype)) return rc;
+  if (yp_dtype != dout_dtype && yp_dtype != MOE_DTYPE_F32)
+    return fail(MOE_ERR_ARG, "%s: rows of type %d with results of type %d", me, yp_dtype, dout_dtype);
+  if (!dyp && !dwts) return fail(MOE_ERR_ARG, "%s: dyp and dwts are both null", me);
+  if (T > 0 && (!dout || !inv || !wts || (dwts && !yp))) return fail(MOE_ERR_ARG, "%s: null pointer", me);
+  if (dyp && (dyp == yp || dyp == dout)) return fail(MOE_ERR_ARG, "%s: dyp overlaps an input", me);
+  if (int rc = check_stride(me, "dout", dout_stride, T, H, false)) return rc;
+  if (int rc = check_stride(me, "yp", yp_stride, (int64_t)T * k, H, false)) return rc;
+  if (int rc = check_stride(me, "dyp", dyp_stride, dyp ? (int64_t)T * k : 0, H, true)) return rc;
+  if (T == 0) return MOE_OK;
+  const size_t ys = dtype_size(yp_dtype);
+  const bool vec = H % 8 == 0 && rows16(dout, dout_stride, dtype_size(dout_dtype)) &&
+                   (!dwts || rows16(yp, yp_stride, ys)) && rows16(dyp, dyp_stride, ys);
+  note_launch();
+  return by_types(yp_dtype, dout_dtype, [&](auto* y, auto* o) {
+    using YT = std::remove_pointer_t<decltype(y)>;
+    using OT = std::remove_pointer_t<decltype(o)>;
+    auto kern = vec ? combine_backward_kernel<YT, OT, true> : combine_backward_kernel<YT, OT, false>;
+    return check_cuda(launch_pdl(kern, dim3(T), dim3(row_threads(H, kRowThreads)), 0,
+                                 reinterpret_cast<cudaStream_t>(stream), static_cast<const OT*>(dout), dout_stride,
+                                 static_cast<const YT*>(yp), yp_stride, inv, wts, k, T * k, H, static_cast<YT*>(dyp),
+                                 dyp_stride, dwts),
+                      "combine_backward_kernel");
+  });
+}
+
+MOE_API int moe_route_topk_backward(const int32_t* idx, const float* wts, const float* dwts, int T, int E, int k,
+                                    void* dlogits, int64_t dlogits_stride, int dtype, moe_stream_t stream) {
+  const char* me = "moe_route_topk_backward";
+  if (T < 0 || k < 1 || k > E) return fail(MOE_ERR_ARG, "%s: bad sizes T=%d E=%d k=%d", me, T, E, k);
+  if (E > kMaxExperts) return fail(MOE_ERR_SHAPE, "%s: E=%d exceeds %d", me, E, kMaxExperts);
+  if ((int64_t)T * k > INT32_MAX) return fail(MOE_ERR_SHAPE, "%s: T*k exceeds 2^31-1", me);
+  if (int rc = check_dtype(me, dtype)) return rc;
+  if (T > 0 && (!idx || !wts || !dwts || !dlogits)) return fail(MOE_ERR_ARG, "%s: null pointer", me);
+  if (int rc = check_stride(me, "dlogits", dlogits_stride, T, E, true)) return rc;
+  if (T == 0) return MOE_OK;
+  note_launch();
+  return by_types(dtype, dtype, [&](auto* l, auto*) {
+    using LT = std::remove_pointer_t<decltype(l)>;
+    return check_cuda(launch_pdl(route_backward_kernel<LT>, dim3(ceil_div(T, kRouterWarps)), dim3(32 * kRouterWarps), 0,
+                                 reinterpret_cast<cudaStream_t>(stream), idx, wts, dwts, T, E, k,
+                                 static_cast<LT*>(dlogits), dlogits_stride),
+                      "route_backward_kernel");
+  });
+}
