@@ -93,6 +93,13 @@ def _load() -> ctypes.CDLL:
 
 lib = _load()
 
+try:
+    from . import _rows            # native argument marshalling of the row operators
+except ImportError as e:
+    raise ImportError(f"the native binding _rows.so is missing or does not load ({e}); build it with "
+                      "`python quantized_mixture_experts_grouped_b200/build.py`") from e
+_rows.set_error(MoeError)
+
 
 def _err(rc: int):
     if rc != MOE_OK:
@@ -210,153 +217,36 @@ def moe_bf16_layer(x, logits, k: int, w13, w2, H: int, I: int, idx, wts, ws, out
 
 
 # ---- rows sorted by expert and back, the router's gradient, norms around a block. These calls take
-# the sizes, types and row strides from the tensors and check them here (MoeError, MOE_ERR_ARG);
-# every tensor lives on one CUDA device, whose current stream is the default.
-
-_ROW_DTYPES = {torch.bfloat16: MOE_DTYPE_BF16, torch.float16: MOE_DTYPE_F16, torch.float32: MOE_DTYPE_F32}
-
-
-class _Call:
-    """The checked tensors of one call: the device and stream they share."""
-
-    def __init__(self, name: str):
-        self.name, self.device = name, None
-
-    def refuse(self, what: str):
-        raise MoeError(MOE_ERR_ARG, f"{self.name}: {what}")
-
-    def _tensor(self, t, what: str):
-        if not isinstance(t, torch.Tensor):
-            self.refuse(f"{what} is not a tensor")
-        if t.device.type != "cuda":
-            self.refuse(f"{what} is not on a CUDA device")
-        if self.device is None:
-            self.device = t.device
-        elif t.device != self.device:
-            self.refuse(f"{what} is on {t.device}, other tensors on {self.device}")
-
-    def rows(self, t, what: str, n: int | None = None, width: int | None = None, dtype=None):
-        """Rows [n][width] with neighbouring values: (pointer, row stride, type code)."""
-        if not isinstance(t, torch.Tensor) or t.dim() != 2:
-            self.refuse(f"{what} is not a matrix of rows")
-        if (n is not None and t.shape[0] != n) or (width is not None and t.shape[1] != width):
-            self.refuse(f"{what} is {tuple(t.shape)}, expected ({n}, {width})")
-        if t.dtype not in _ROW_DTYPES or (dtype is not None and t.dtype != dtype):
-            self.refuse(f"{what} is {t.dtype}")
-        if t.shape[1] > 1 and t.stride(1) != 1 and t.shape[0]:
-            self.refuse(f"the values of a row of {what} are not neighbours")
-        self._tensor(t, what)
-        return _p(t), t.stride(0) if t.shape[0] > 1 else t.shape[1], _ROW_DTYPES[t.dtype]
-
-    def dense(self, t, what: str, shape, dtype):
-        """A contiguous tensor of this shape and type: its pointer."""
-        if not isinstance(t, torch.Tensor) or tuple(t.shape) != tuple(shape):
-            self.refuse(f"{what} is not a tensor of shape {tuple(shape)}")
-        if t.dtype != dtype:
-            self.refuse(f"{what} is {t.dtype}, expected {dtype}")
-        if not t.is_contiguous():
-            self.refuse(f"{what} is not contiguous")
-        self._tensor(t, what)
-        return _p(t)
-
-    def vector(self, t, what: str, width: int, dtype):
-        return None if t is None else self.dense(t, what, (width,), dtype)
-
-    def gate(self, g, what: str, T: int, H: int, dtype, sums: bool = False):
-        """A gate that broadcasts over the rows, (pointer, stride, mode): [H] per channel, fp32 [T][1]
-        per token, [T][H] per value; sums: its gradient (per channel fp32)."""
-        if g is None:
-            return None, 0, MOE_GATE_NONE
-        if isinstance(g, torch.Tensor) and g.dim() == 1:
-            return self.dense(g, what, (H,), torch.float32 if sums else dtype), 0, MOE_GATE_CHANNEL
-        if isinstance(g, torch.Tensor) and g.shape == (T, 1) and g.dtype == torch.float32:
-            return self.dense(g, what, (T, 1), torch.float32), 0, MOE_GATE_TOKEN
-        return *self.rows(g, what, T, H, dtype)[:2], MOE_GATE_FULL
-
-    def run(self, fn, *args, stream=None):
-        with torch.cuda.device(self.device):
-            if stream is None:
-                stream = torch.cuda.current_stream(self.device)
-            elif stream.device != self.device:
-                self.refuse(f"the stream is on {stream.device}, the tensors on {self.device}")
-            _err(fn(*args, ctypes.c_void_p(stream.cuda_stream)))
+# the sizes, types and row strides from the tensors and check them (MoeError, MOE_ERR_ARG) in the
+# native module _rows (csrc/binding.cpp); every tensor lives on one CUDA device, whose current
+# stream is the default.
 
 
 def moe_dispatch(x, idx, E: int, counts, offsets, perm, inv, xp, stream=None):
     """Sorts the token-expert pairs of idx (int32 [T][k]) by expert and writes each token's row of x
     [T][H] to its pairs' rows of xp [T*k][H]. counts [E], offsets [E+1], perm [T*k], inv [T][k] (int32)."""
-    c = _Call("moe_dispatch")
-    T, k = _pairs(c, idx, "idx")
-    xr = c.rows(x, "x", T)
-    H, i32 = x.shape[1], torch.int32
-    pr = c.rows(xp, "xp", T * k, H, x.dtype)
-    args = (c.dense(counts, "counts", (E,), i32), c.dense(offsets, "offsets", (E + 1,), i32),
-            c.dense(perm, "perm", (T * k,), i32), c.dense(inv, "inv", (T, k), i32))
-    c.run(lib.moe_dispatch, xr[0], xr[1], xr[2], _p(idx), T, H, E, k, *args, pr[0], pr[1], stream=stream)
+    _rows.dispatch(x, idx, E, counts, offsets, perm, inv, xp, stream)
 
 
 def moe_dispatch_backward(dxp, inv, dx, stream=None):
     """dx[t] = sum of the rows of dxp [T*k][H] that moe_dispatch filled from token t."""
-    c = _Call("moe_dispatch_backward")
-    T, k = _pairs(c, inv, "inv")
-    dr = c.rows(dx, "dx", T)
-    H = dx.shape[1]
-    pr = c.rows(dxp, "dxp", T * k, H, dx.dtype)
-    c.run(lib.moe_dispatch_backward, pr[0], pr[1], pr[2], _p(inv), T, H, k, dr[0], dr[1], stream=stream)
+    _rows.dispatch_backward(dxp, inv, dx, stream)
 
 
 def moe_combine(yp, inv, wts, out, stream=None):
     """out[t] = sum_j wts[t][j] * yp[inv[t][j]]; yp [T*k][H] of out's type or fp32, wts fp32 [T][k]."""
-    c = _Call("moe_combine")
-    T, k = _pairs(c, inv, "inv")
-    orow = c.rows(out, "out", T)
-    H = out.shape[1]
-    yr = c.rows(yp, "yp", T * k, H)
-    w = c.dense(wts, "wts", (T, k), torch.float32)
-    c.run(lib.moe_combine, yr[0], yr[1], yr[2], _p(inv), w, T, H, k, orow[0], orow[1], orow[2], stream=stream)
+    _rows.combine(yp, inv, wts, out, stream)
 
 
 def moe_combine_backward(dout, yp, inv, wts, dyp=None, dwts=None, stream=None):
     """Gradients of moe_combine: dyp (rows like yp), dwts (fp32 [T][k]); either may be None. yp may be
     None when dwts is."""
-    c = _Call("moe_combine_backward")
-    T, k = _pairs(c, inv, "inv")
-    dr = c.rows(dout, "dout", T)
-    H = dout.shape[1]
-    yr = (None, 0, None) if yp is None else c.rows(yp, "yp", T * k, H)
-    gr = (None, 0, yr[2]) if dyp is None else c.rows(dyp, "dyp", T * k, H, None if yp is None else yp.dtype)
-    w = c.dense(wts, "wts", (T, k), torch.float32)
-    dw = None if dwts is None else c.dense(dwts, "dwts", (T, k), torch.float32)
-    ydt = gr[2] if gr[2] is not None else dr[2]
-    c.run(lib.moe_combine_backward, dr[0], dr[1], dr[2], yr[0], yr[1], ydt, _p(inv), w, T, H, k, gr[0], gr[1], dw,
-          stream=stream)
+    _rows.combine_backward(dout, yp, inv, wts, dyp, dwts, stream)
 
 
 def moe_route_topk_backward(idx, wts, dwts, dlogits, stream=None):
     """Gradient of moe_route_topk's weights towards the logits: dlogits [T][E], 0 where not chosen."""
-    c = _Call("moe_route_topk_backward")
-    T, k = _pairs(c, idx, "idx")
-    lr = c.rows(dlogits, "dlogits", T)
-    w, d = (c.dense(t, n, (T, k), torch.float32) for t, n in ((wts, "wts"), (dwts, "dwts")))
-    c.run(lib.moe_route_topk_backward, _p(idx), w, d, T, dlogits.shape[1], k, lr[0], lr[1], lr[2], stream=stream)
-
-
-def _pairs(c: _Call, t, what: str):
-    """(T, k) of an int32 [T][k] tensor."""
-    if not isinstance(t, torch.Tensor) or t.dim() != 2:
-        c.refuse(f"{what} is not an int32 [T][k] tensor")
-    c.dense(t, what, t.shape, torch.int32)
-    return t.shape
-
-
-def _ws(c: _Call, ws):
-    """(pointer, bytes) of a workspace that may be None."""
-    if ws is None:
-        return None, 0
-    c._tensor(ws, "ws")
-    if not ws.is_contiguous():
-        c.refuse("ws is not contiguous")
-    return _p(ws), ws.numel() * ws.element_size()
+    _rows.route_topk_backward(idx, wts, dwts, dlogits, stream)
 
 
 def moe_norm_workspace_bytes(T: int, H: int) -> int:
@@ -367,64 +257,26 @@ def moe_norm_workspace_bytes(T: int, H: int) -> int:
 
 def moe_norm_pre(h, w, eps: float, x, stream=None):
     """x = h / sqrt(mean(h^2) + eps) * w, row by row; w [H] or None."""
-    c = _Call("moe_norm_pre")
-    hr = c.rows(h, "h")
-    T, H = h.shape
-    xr = c.rows(x, "x", T, H, h.dtype)
-    c.run(lib.moe_norm_pre, hr[0], hr[1], hr[2], c.vector(w, "w", H, h.dtype), eps, T, H, xr[0], xr[1], stream=stream)
+    _rows.norm_pre(h, w, eps, x, stream)
 
 
 def moe_norm_pre_backward(dx, h, w, eps: float, dh, dres=None, dw=None, ws=None, stream=None):
     """Gradients of moe_norm_pre: dh (plus the residual path's dres), dw (fp32 [H]). dw needs ws, a
-    workspace of moe_norm_workspace_bytes."""
-    c = _Call("moe_norm_pre_backward")
-    hr = c.rows(h, "h")
-    T, H = h.shape
-    xr, dr = c.rows(dx, "dx", T, H, h.dtype), c.rows(dh, "dh", T, H, h.dtype)
-    rr = (None, 0) if dres is None else c.rows(dres, "dres", T, H, h.dtype)
-    c.run(lib.moe_norm_pre_backward, xr[0], xr[1], hr[0], hr[1], hr[2], c.vector(w, "w", H, h.dtype), eps, T, H, rr[0],
-          rr[1], dr[0], dr[1], c.vector(dw, "dw", H, torch.float32), *_ws(c, ws), stream=stream)
-
-
-def _post(c: _Call, h, h_out, w, gate, norm_y, w_next, x_next):
-    """The arguments that moe_norm_post and moe_combine_norm_post share."""
-    hr = c.rows(h, "h")
-    T, H = h.shape
-    orow = c.rows(h_out, "h_out", T, H, h.dtype)
-    xr = (None, 0) if x_next is None else c.rows(x_next, "x_next", T, H, h.dtype)
-    if w is not None and not norm_y:
-        c.refuse("w without norm_y")
-    if w_next is not None and x_next is None:
-        c.refuse("w_next without x_next")
-    flags = (MOE_NORM_Y if norm_y else 0) | (MOE_NORM_NEXT if x_next is not None else 0)
-    return (T, H, flags, hr, c.vector(w, "w", H, h.dtype), c.gate(gate, "gate", T, H, h.dtype), orow,
-            c.vector(w_next, "w_next", H, h.dtype), xr)
+    workspace of moe_norm_workspace_bytes. dh may be dres."""
+    _rows.norm_pre_backward(dx, h, w, eps, dh, dres, dw, ws, stream)
 
 
 def moe_norm_post(y, h, h_out, eps: float, alpha: float = 1.0, norm_y: bool = True, w=None, gate=None, w_next=None,
                   x_next=None, stream=None):
     """h_out = alpha * h + gate * u with u = rms(y) * w (norm_y) or y, and with x_next given
     x_next = rms(h_out) * w_next. gate: None, [H], fp32 [T][1] or [T][H]. h_out may be h."""
-    c = _Call("moe_norm_post")
-    T, H, flags, hr, wp, g, orow, wn, xr = _post(c, h, h_out, w, gate, norm_y, w_next, x_next)
-    yr = c.rows(y, "y", T, H, h.dtype)
-    c.run(lib.moe_norm_post, yr[0], yr[1], hr[0], hr[1], hr[2], wp, *g, alpha, eps, T, H, flags, orow[0], orow[1], wn,
-          xr[0], xr[1], stream=stream)
+    _rows.norm_post(y, h, h_out, eps, alpha, norm_y, w, gate, w_next, x_next, stream)
 
 
 def moe_combine_norm_post(yp, inv, wts, h, h_out, eps: float, alpha: float = 1.0, norm_y: bool = True, w=None,
                           gate=None, w_next=None, x_next=None, y_out=None, stream=None):
     """moe_combine and moe_norm_post in one launch; y_out (optional) keeps the combined rows."""
-    c = _Call("moe_combine_norm_post")
-    T, H, flags, hr, wp, g, orow, wn, xr = _post(c, h, h_out, w, gate, norm_y, w_next, x_next)
-    if _pairs(c, inv, "inv")[0] != T:
-        c.refuse(f"inv has {inv.shape[0]} tokens, h {T}")
-    k = inv.shape[1]
-    yr = c.rows(yp, "yp", T * k, H)
-    kr = (None, 0) if y_out is None else c.rows(y_out, "y_out", T, H, h.dtype)
-    c.run(lib.moe_combine_norm_post, yr[0], yr[1], yr[2], _p(inv), c.dense(wts, "wts", (T, k), torch.float32), k,
-          hr[0], hr[1], hr[2], wp, *g, alpha, eps, T, H, flags, orow[0], orow[1], wn, xr[0], xr[1], kr[0], kr[1],
-          stream=stream)
+    _rows.combine_norm_post(yp, inv, wts, h, h_out, eps, alpha, norm_y, w, gate, w_next, x_next, y_out, stream)
 
 
 def moe_norm_post_backward(dh_out, y, dh, dy, eps: float, alpha: float = 1.0, norm_y: bool = True, w=None, dw=None,
@@ -433,27 +285,8 @@ def moe_norm_post_backward(dh_out, y, dh, dy, eps: float, alpha: float = 1.0, no
     """Gradients of moe_norm_post: dh, dy, and where given dw, dw_next (fp32 [H]) and dgate (fp32 [H],
     fp32 [T][1] or rows). With dx_next given, h_out is the forward's output. Gradients of vectors need
     ws, a workspace of moe_norm_workspace_bytes. dh may be dh_out."""
-    c = _Call("moe_norm_post_backward")
-    dr = c.rows(dh_out, "dh_out")
-    T, H = dh_out.shape
-    dt = dh_out.dtype
-    yr, hr, gy = c.rows(y, "y", T, H, dt), c.rows(dh, "dh", T, H, dt), c.rows(dy, "dy", T, H, dt)
-    nxt = dx_next is not None
-    if not nxt and (w_next is not None or dw_next is not None or h_out is not None):
-        c.refuse("h_out, w_next or dw_next without dx_next")
-    if not norm_y and w is not None:
-        c.refuse("w without norm_y")
-    orow = (None, 0) if not nxt else c.rows(h_out, "h_out", T, H, dt)
-    xr = (None, 0) if not nxt else c.rows(dx_next, "dx_next", T, H, dt)
-    g = c.gate(gate, "gate", T, H, dt)
-    dg = c.gate(dgate, "dgate", T, H, dt, sums=True)
-    if dgate is not None and dg[2] != g[2]:
-        c.refuse("dgate has another form than gate")
-    flags = (MOE_NORM_Y if norm_y else 0) | (MOE_NORM_NEXT if nxt else 0)
-    c.run(lib.moe_norm_post_backward, dr[0], dr[1], yr[0], yr[1], dr[2], c.vector(w, "w", H, dt), *g, alpha, eps, T, H,
-          flags, orow[0], orow[1], c.vector(w_next, "w_next", H, dt), xr[0], xr[1], hr[0], hr[1], gy[0], gy[1],
-          c.vector(dw, "dw", H, torch.float32), dg[0], dg[1], c.vector(dw_next, "dw_next", H, torch.float32),
-          *_ws(c, ws), stream=stream)
+    _rows.norm_post_backward(dh_out, y, dh, dy, eps, alpha, norm_y, w, dw, gate, dgate, h_out, w_next, dx_next,
+                             dw_next, ws, stream)
 
 
 def moe_noalloc_status(stream=None) -> int:

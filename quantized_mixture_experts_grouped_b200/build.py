@@ -6,7 +6,9 @@
 
 Each .cu file is compiled to an object under _build/ (in parallel, skipped when up to date),
 then linked into a shared library next to this file. The CUDA runtime is linked statically so
-the library does not depend on the runtime that torch happens to ship.
+the library does not depend on the runtime that torch happens to ship. csrc/binding.cpp, the native
+half of the Python binding, becomes the extension module _rows.so (g++, torch's headers), linked
+against that library.
 """
 from __future__ import annotations
 
@@ -22,6 +24,7 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libmoe_w4a16.so")
+BINDING = os.path.join(PKG, "_rows.so")
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 NVCC_FLAGS = ["-std=c++17", "-O3", "-lineinfo", *ARCH, "-Xcompiler", "-fPIC,-fvisibility=hidden",
               "-I", INCLUDE, "-I", CSRC, "-prec-div=true", "-prec-sqrt=true", "-ftz=false", "-Xptxas", "-warn-spills"]
@@ -69,7 +72,35 @@ def build(force: bool = False, verbose: bool = False, extra: list[str] | None = 
             print(" ".join(cmd), flush=True)
         subprocess.check_call(cmd)
         os.replace(tmp, LIB)
+    _build_binding(force, verbose)
     return LIB
+
+
+def _build_binding(force: bool, verbose: bool) -> None:
+    src = os.path.join(CSRC, "binding.cpp")
+    header = os.path.join(INCLUDE, "moe_w4a16.h")
+    if not force and os.path.exists(BINDING) and os.path.getmtime(BINDING) >= max(os.path.getmtime(src),
+                                                                                 os.path.getmtime(header)):
+        return
+    import sysconfig
+
+    import torch
+    root = os.path.dirname(torch.__file__)
+    cuda = os.environ.get("CUDA_HOME", "/usr/local/cuda")
+    tmp = BINDING + f".tmp{os.getpid()}"
+    cmd = ["g++", "-std=c++17", "-O2", "-fPIC", "-shared", "-fvisibility=hidden",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", "-I", INCLUDE,
+           "-isystem", sysconfig.get_paths()["include"], "-isystem", os.path.join(root, "include"),
+           "-isystem", os.path.join(root, "include", "torch", "csrc", "api", "include"),
+           "-isystem", os.path.join(cuda, "include"), src, "-o", tmp, "-L", PKG, "-l:libmoe_w4a16.so",
+           "-L", os.path.join(root, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10_cuda", "-lc10",
+           "-Wl,-rpath,$ORIGIN"]      # torch's own libraries are loaded by then
+    if verbose:
+        print(" ".join(cmd), flush=True)
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed on binding.cpp:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, BINDING)
 
 
 if __name__ == "__main__":
