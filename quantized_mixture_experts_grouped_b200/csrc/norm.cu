@@ -280,6 +280,190 @@ __global__ void __launch_bounds__(MAXT) norm_backward_kernel(const BackArgs a) {
   }
 }
 
+// The same gradient for rows of 16-byte words whose tensors fit a ring of stages in shared memory:
+// each thread copies its own words of the next rows (cp.async) while it works on this one, so the
+// loads of several rows stay in flight across the two block-wide sums of a row. A thread only reads
+// words it copied itself: the ring needs no barrier. The weights and the per-channel gate stay in
+// registers. T = 8192, H = 4096, bf16, gate per value, next norm: 234 us with loads at the top of
+// each row, when a row's loads waited for the sums of the row before.
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+
+template <typename T>
+__device__ __forceinline__ void ring_load(const unsigned char* s, int nt, float (&f)[8]) {
+  Raw8<T> r;
+  uint4* q = reinterpret_cast<uint4*>(&r);
+#pragma unroll
+  for (int i = 0; i < (int)sizeof(T) / 2; ++i) q[i] = *reinterpret_cast<const uint4*>(s + (size_t)i * nt * 16);
+  to_float(r, f);
+}
+
+constexpr int kRingStages = 4;
+constexpr int kRingBytes = 224 * 1024 - 4096;        // of an SM's 228 KB, for all its blocks
+
+template <typename T, int MAXT>
+__global__ void __launch_bounds__(MAXT, MAXT <= 256 ? 2 : 1) norm_backward_ring_kernel(const BackArgs a, int stages,
+                                                                                       int stage_bytes) {
+  extern __shared__ __align__(16) unsigned char ring[];
+  __shared__ float buf[2][32 * 3];
+  int flip = 0;
+  constexpr int W = (int)sizeof(T) / 2;              // 16-byte words per thread and tensor
+  const int nt = blockDim.x, tid = threadIdx.x, H = a.H, n0 = tid * 8;
+  const bool mine = n0 < H, full = a.gate_mode == MOE_GATE_FULL;
+  const int region = nt * 16 * W;
+  // where each tensor's words lie in a stage
+  const int at_y = a.dho ? region : 0, at_h = at_y + (a.has_y ? region : 0), at_x = at_h + (a.next ? region : 0),
+            at_g = at_x + (a.next ? region : 0);
+  unsigned char* own = ring + tid * 16;
+  if (!mine)
+    for (int o = 0; o < stages * stage_bytes; o += nt * 16) *reinterpret_cast<uint4*>(own + o) = make_uint4(0, 0, 0, 0);
+  const uint32_t own_s = (uint32_t)__cvta_generic_to_shared(own);
+  auto words = [&](uint32_t dst, const void* base, int64_t ld, int64_t t) {
+    const char* src = reinterpret_cast<const char*>(static_cast<const T*>(base) + t * ld + n0);
+#pragma unroll
+    for (int i = 0; i < W; ++i) copy16(dst + i * nt * 16, src + i * 16);
+  };
+  auto issue = [&](int64_t t, int stage) {
+    if (t < a.T && mine) {
+      const uint32_t d = own_s + stage * stage_bytes;
+      if (a.dho) words(d, a.dho, a.lddho, t);
+      if (a.has_y) words(d + at_y, a.y, a.ldy, t);
+      if (a.next) {
+        words(d + at_h, a.ho, a.ldho, t);
+        words(d + at_x, a.dx, a.lddx, t);
+      }
+      if (full) words(d + at_g, a.gate, a.ldg, t);
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+  pdl_begin();
+  for (int i = 0; i < stages - 1; ++i) issue((int64_t)blockIdx.x + (int64_t)i * gridDim.x, i);
+  const float inv_h = 1.f / (float)H;
+  // ones where there is no weight (also past H, where everything else is 0)
+  Raw8<T> w, wn, gc;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) w.v[e] = wn.v[e] = gc.v[e] = RowType<T>::from(1.f);
+  if (a.norm_y && a.w) w = load_raw<true>(static_cast<const T*>(a.w), 0, nt, tid, H);
+  if (a.next && a.w_next) wn = load_raw<true>(static_cast<const T*>(a.w_next), 0, nt, tid, H);
+  if (a.gate_mode == MOE_GATE_CHANNEL) gc = load_raw<true>(static_cast<const T*>(a.gate), 0, nt, tid, H);
+  float sw[8], sg[8], sn[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) sw[e] = sg[e] = sn[e] = 0.f;
+  int stage = 0;
+  for (int64_t t = blockIdx.x; t < a.T; t += gridDim.x) {
+    issue(t + (int64_t)(stages - 1) * gridDim.x, stage == 0 ? stages - 1 : stage - 1);
+    // this row's copies are done when at most the stages - 1 groups after it are under way
+    if (stages == 4) asm volatile("cp.async.wait_group 3;" ::: "memory");
+    else if (stages == 3) asm volatile("cp.async.wait_group 2;" ::: "memory");
+    else asm volatile("cp.async.wait_group 1;" ::: "memory");
+    const unsigned char* s0 = own + (size_t)stage * stage_bytes;
+    stage = stage + 1 == stages ? 0 : stage + 1;
+    float d[8], y[8], h[8], x[8];
+    float s[3] = {0.f, 0.f, 0.f};     // sum h'^2, sum w' dx h', sum y^2
+    if (a.next) {
+      ring_load<T>(s0 + at_h, nt, h);
+      ring_load<T>(s0 + at_x, nt, x);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        s[0] = fmaf(h[e], h[e], s[0]);
+        s[1] = fmaf(RowType<T>::to(wn.v[e]) * x[e], h[e], s[1]);
+      }
+    }
+    if (a.has_y) ring_load<T>(s0 + at_y, nt, y);
+    if (a.norm_y) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) s[2] = fmaf(y[e], y[e], s[2]);
+    }
+    if (a.next || a.norm_y) {
+      block_sums<3>(s, buf[flip]);
+      flip ^= 1;
+    }
+    if (a.dho) {
+      ring_load<T>(s0, nt, d);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) d[e] = 0.f;
+    }
+    if (a.next) {
+      const float r = rsqrtf(s[0] * inv_h + a.eps);
+      const float m = s[1] * inv_h * r;              // mean(w' dx n), n = h' r
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const float n = h[e] * r;
+        d[e] += r * (RowType<T>::to(wn.v[e]) * x[e] - n * m);
+        sn[e] = fmaf(x[e], n, sn[e]);
+      }
+    }
+    float o[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) o[e] = a.alpha * d[e];
+    store8<true>(static_cast<T*>(a.dh) + t * a.lddh, 0, nt, tid, H, o);
+    if (!a.has_y) continue;
+    const float q = a.norm_y ? rsqrtf(s[2] * inv_h + a.eps) : 1.f;
+    float z[2] = {0.f, 0.f};          // sum w du n, sum d u
+    float g[8], u[8];
+    if (full) {
+      ring_load<T>(s0 + at_g, nt, g);
+    } else if (a.gate_mode == MOE_GATE_TOKEN) {
+      const float v = static_cast<const float*>(a.gate)[t];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) g[e] = v;
+    } else {
+      to_float(gc, g);
+    }
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      y[e] *= q;
+      u[e] = d[e] * (y[e] * RowType<T>::to(w.v[e]));   // d u
+      d[e] *= g[e];                                    // du
+    }
+    if (full) {
+      if (a.dgate) store8<true>(static_cast<T*>(a.dgate) + t * a.lddg, 0, nt, tid, H, u);
+    } else if (a.gate_mode == MOE_GATE_CHANNEL) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) sg[e] += u[e];
+    } else if (a.gate_mode == MOE_GATE_TOKEN) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) z[1] += u[e];
+    }
+    if (a.norm_y) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        sw[e] = fmaf(d[e], y[e], sw[e]);
+        d[e] *= RowType<T>::to(w.v[e]);
+        z[0] = fmaf(d[e], y[e], z[0]);
+      }
+    }
+    if (a.norm_y || a.gate_mode == MOE_GATE_TOKEN) {
+      block_sums<2>(z, buf[flip]);
+      flip ^= 1;
+    }
+    if (a.gate_mode == MOE_GATE_TOKEN && a.dgate && tid == 0) static_cast<float*>(a.dgate)[t] = z[1];
+    if (a.norm_y) {
+      const float m = z[0] * inv_h;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) d[e] = q * (d[e] - y[e] * m);
+    }
+    store8<true>(static_cast<T*>(a.dy) + t * a.lddy, 0, nt, tid, H, d);
+  }
+  if (!mine) return;
+  auto leave = [&](float* out, int i, const float(&v)[8]) {
+    if (!out) return;
+    float4* o = reinterpret_cast<float4*>((gridDim.x == 1 ? out : a.part + ((int64_t)blockIdx.x * kSums + i) * H) + n0);
+    if (reinterpret_cast<uintptr_t>(o) & 15) {         // a caller's vector on any boundary
+#pragma unroll
+      for (int e = 0; e < 8; ++e) reinterpret_cast<float*>(o)[e] = v[e];
+    } else {
+      o[0] = make_float4(v[0], v[1], v[2], v[3]);
+      o[1] = make_float4(v[4], v[5], v[6], v[7]);
+    }
+  };
+  leave(a.dw, 0, sw);
+  leave(a.gate_mode == MOE_GATE_CHANNEL ? static_cast<float*>(a.dgate) : nullptr, 1, sg);
+  leave(a.dw_next, 2, sn);
+}
+
 // Adds the blocks' partial sums: 32 columns by 32 runs of blocks per block, each run in block
 // order, then the runs in order.
 __global__ void __launch_bounds__(1024) norm_sums_kernel(const float* __restrict__ part, int blocks, int H, float* o0,
@@ -339,8 +523,7 @@ int norm_sms() {
 // Blocks of the backward kernel never exceed this, so that the workspace's size does not depend on
 // the device.
 constexpr int kMaxBlocks = 592;
-int back_blocks(int T, int nt) {
-  const int per_sm = nt <= 256 ? 2 : 1;
+int back_blocks(int T, int per_sm) {
   const int b = norm_sms() * per_sm;
   return T < b ? T : b < kMaxBlocks ? b : kMaxBlocks;
 }
@@ -425,7 +608,14 @@ int launch_back(const char* me, BackArgs& a, int dtype, bool vec, void* ws, size
     return MOE_OK;
   }
   const Shape sh = shape_of(a.H, 1024);
-  const int blocks = back_blocks(a.T, sh.nt);
+  // the ring takes as many stages as fit beside the other block of the SM
+  const int per_sm = sh.nt <= 256 ? 2 : 1;
+  const int tensors = (a.dho ? 1 : 0) + (a.has_y ? 1 : 0) + (a.next ? 2 : 0) + (a.gate_mode == MOE_GATE_FULL ? 1 : 0);
+  const int stage_bytes = tensors * sh.nt * 8 * (int)dtype_size(dtype);
+  const int fit = kRingBytes / per_sm / stage_bytes;
+  const int stages = fit < kRingStages ? fit : kRingStages;
+  const bool use_ring = vec && sh.nc == 1 && stages >= 2;
+  const int blocks = back_blocks(a.T, per_sm);
   if (any && blocks > 1) {
     const size_t need = norm_ws(a.T, a.H);
     if (!ws || ws_bytes < need)
@@ -436,6 +626,15 @@ int launch_back(const char* me, BackArgs& a, int dtype, bool vec, void* ws, size
   note_launch();
   int rc = by_type(dtype, [&](auto* p) {
     using T = std::remove_pointer_t<decltype(p)>;
+    if (use_ring) {
+      auto ring = sh.nt <= 256 ? norm_backward_ring_kernel<T, 256>
+                               : sh.nt <= 512 ? norm_backward_ring_kernel<T, 512> : norm_backward_ring_kernel<T, 1024>;
+      const size_t smem = (size_t)stages * stage_bytes;
+      if (int e = check_cuda(cudaFuncSetAttribute(ring, cudaFuncAttributeMaxDynamicSharedMemorySize, kRingBytes), me))
+        return e;
+      return check_cuda(launch_pdl(ring, dim3(blocks), dim3(sh.nt), smem, s, a, stages, stage_bytes),
+                        "norm_backward_ring_kernel");
+    }
     auto kern = vec ? back_kernel<T, true>(sh) : back_kernel<T, false>(sh);
     return check_cuda(launch_pdl(kern, dim3(blocks), dim3(sh.nt), 0, s, a), "norm_backward_kernel");
   });

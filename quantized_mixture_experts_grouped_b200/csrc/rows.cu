@@ -41,9 +41,10 @@ __global__ void __launch_bounds__(kSortThreads) sort_pairs_kernel(const int32_t*
   __shared__ int32_t first[kMaxExperts];
   __shared__ int32_t wsum[kMaxExperts / 32];
   cg::cluster_group cluster = cg::this_cluster();
-  const int rank = cluster.block_rank(), nblk = cluster.num_blocks();
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, nw = blockDim.x >> 5;
-  const int per_block = (int)(((int64_t)P + nblk - 1) / nblk);
+  const int rank = cluster.block_rank();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  constexpr int nw = kSortThreads / 32;
+  const int per_block = (int)(((int64_t)P + kSortCluster - 1) / kSortCluster);
   const int per_warp = (per_block + 32 * nw - 1) / (32 * nw) * 32;
   const int64_t b0 = (int64_t)rank * per_block, b1 = min(b0 + per_block, (int64_t)P);
   const int64_t w0 = b0 + (int64_t)warp * per_warp, w1 = min(w0 + per_warp, b1);
@@ -58,26 +59,44 @@ __global__ void __launch_bounds__(kSortThreads) sort_pairs_kernel(const int32_t*
     __syncwarp();
   }
   __syncthreads();
-  for (int e = threadIdx.x; e < E; e += blockDim.x) {
-    int run = 0;
-    for (int w = 0; w < nw; ++w) {
-      const int c = wcount[w][e];
-      wcount[w][e] = run;
-      run += c;
+  // prefix of the warps' counts per expert: eight neighbouring lanes share an expert, four warps each
+  for (int i = threadIdx.x; i < (E + 3) / 4 * 32; i += kSortThreads) {
+    const int e = i >> 3, part = i & 7;
+    int c[4], sum = 0;
+#pragma unroll
+    for (int w = 0; w < 4; ++w) {
+      c[w] = e < E ? wcount[part * 4 + w][e] : 0;
+      sum += c[w];
     }
-    total[e] = run;
+    int run = sum;
+#pragma unroll
+    for (int o = 1; o < 8; o <<= 1) {
+      const int v = __shfl_up_sync(0xffffffffu, run, o, 8);
+      if (part >= o) run += v;
+    }
+    if (e < E && part == 7) total[e] = run;
+    run -= sum;
+#pragma unroll
+    for (int w = 0; w < 4; ++w) {
+      if (e < E) wcount[part * 4 + w][e] = run;
+      run += c[w];
+    }
   }
   cluster.sync();
   // each block: pairs of expert e in the blocks before it, and in all of them
   int all = 0, before = 0;
   const int e0 = threadIdx.x;
   if (e0 < E) {
-    for (int r = 0; r < nblk; ++r) {
-      const int c = *cluster.map_shared_rank(&total[e0], r);
-      if (r < rank) before += c;
-      all += c;
+    int c[kSortCluster];
+#pragma unroll
+    for (int r = 0; r < kSortCluster; ++r) c[r] = *cluster.map_shared_rank(&total[e0], r);
+#pragma unroll
+    for (int r = 0; r < kSortCluster; ++r) {
+      if (r < rank) before += c[r];
+      all += c[r];
     }
   }
+  cg::cluster_group::arrival_token done = cluster.barrier_arrive();   // the others' counts are read
   // exclusive prefix over the experts: within a warp, then over the (at most 8) warps that hold one
   int incl = all;
 #pragma unroll
@@ -96,7 +115,7 @@ __global__ void __launch_bounds__(kSortThreads) sort_pairs_kernel(const int32_t*
       if (e0 == E - 1) offsets[E] = incl;
     }
   }
-  cluster.sync();   // also: no block leaves while another reads its counts
+  __syncthreads();
   for (int64_t p0 = w0; p0 < w1; p0 += 32) {
     const int64_t p = p0 + lane;
     int e = p < w1 ? idx[p] : -1;
@@ -111,6 +130,7 @@ __global__ void __launch_bounds__(kSortThreads) sort_pairs_kernel(const int32_t*
     if (p < w1) inv[p] = place;
     if (place >= 0) perm[place] = (int32_t)p;
   }
+  cluster.barrier_wait(std::move(done));   // no block leaves while another reads its counts
 }
 
 // ------------------------------------------------------------------------------------- dispatch
@@ -275,35 +295,41 @@ __global__ void __launch_bounds__(kRowThreads) combine_backward_kernel(const OT*
     int pos[kDots];
 #pragma unroll
     for (int b = 0; b < kDots; ++b) {
+      const bool in = j0 + b < k;
+      pos[b] = in ? it[j0 + b] : -1;
+      w[b] = in ? wt[j0 + b] : 0.f;
       dot[b] = 0.f;
-      const int p = j0 + b < k ? it[j0 + b] : -1;
-      pos[b] = (unsigned)p < (unsigned)P ? p : -1;
-      w[b] = pos[b] >= 0 ? wt[j0 + b] : 0.f;
     }
+#pragma unroll
+    for (int b = 0; b < kDots; ++b)
+      if ((unsigned)pos[b] >= (unsigned)P) pos[b] = -1;
     for (int c = 0; c < chunks; ++c) {
       float d[8];
       load8<VEC>(dout + t * ldo, c, nt, tid, H, d);
       constexpr int B = sizeof(YT) == 2 ? 8 : 4;
 #pragma unroll
       for (int b0 = 0; b0 < kDots; b0 += B) {
-        Raw8<YT> r[B];
+        if (j0 + b0 >= k) break;
         if (dwts) {
+          Raw8<YT> r[B];
+#pragma unroll
+          for (int b = 0; b < B; ++b) {
+            const bool on = pos[b0 + b] >= 0;
+            r[b] = load_raw<VEC>(yp + (int64_t)(on ? pos[b0 + b] : 0) * ldy, c, nt, tid, on ? H : 0);
+          }
 #pragma unroll
           for (int b = 0; b < B; ++b)
-            if (pos[b0 + b] >= 0) r[b] = load_raw<VEC>(yp + (int64_t)pos[b0 + b] * ldy, c, nt, tid, H);
-        }
 #pragma unroll
-        for (int b = 0; b < B; ++b) {
-          if (pos[b0 + b] < 0) continue;
-          if (dyp) {
+            for (int e = 0; e < 8; ++e) dot[b0 + b] = fmaf(d[e], RowType<YT>::to(r[b].v[e]), dot[b0 + b]);
+        }
+        if (dyp) {
+#pragma unroll
+          for (int b = 0; b < B; ++b) {
             float g[8];
 #pragma unroll
             for (int e = 0; e < 8; ++e) g[e] = w[b0 + b] * d[e];
-            store8<VEC>(dyp + (int64_t)pos[b0 + b] * lddy, c, nt, tid, H, g);
-          }
-          if (dwts) {
-#pragma unroll
-            for (int e = 0; e < 8; ++e) dot[b0 + b] = fmaf(d[e], RowType<YT>::to(r[b].v[e]), dot[b0 + b]);
+            const bool on = pos[b0 + b] >= 0;
+            store8<VEC>(dyp + (int64_t)(on ? pos[b0 + b] : 0) * lddy, c, nt, tid, on ? H : 0, g);
           }
         }
       }

@@ -109,7 +109,10 @@ __device__ __forceinline__ void block_sums(float (&v)[N], float* buf) {
 }
 
 // out = sum over j of w[j] * rows[inv[j]] (chunk c of a token), in j order; a choice whose inv is
-// outside [0, P) adds nothing. Eight choices' loads are in flight at a time.
+// outside [0, P) adds nothing. The places and weights of a batch of choices are read before the
+// first of their rows, and the rows before the first is used, so that one token waits for memory
+// twice and not twice per choice (2048 tokens, 8 choices, H = 2048: 44 us when each row waited for
+// its own place).
 template <bool VEC, typename T>
 __device__ __forceinline__ void weighted_rows(const T* rows, int64_t ld, const int32_t* inv, const float* wts, int k,
                                               int P, int c, int nt, int tid, int H, float (&out)[8]) {
@@ -119,20 +122,24 @@ __device__ __forceinline__ void weighted_rows(const T* rows, int64_t ld, const i
   for (int j0 = 0; j0 < k; j0 += B) {
     Raw8<T> r[B];
     float w[B];
-    bool on[B];
+    int p[B];
 #pragma unroll
     for (int b = 0; b < B; ++b) {
-      const int p = j0 + b < k ? inv[j0 + b] : -1;
-      on[b] = (unsigned)p < (unsigned)P;
-      w[b] = on[b] && wts ? wts[j0 + b] : 1.f;
-      if (on[b]) r[b] = load_raw<VEC>(rows + (int64_t)p * ld, c, nt, tid, H);
+      const bool in = j0 + b < k;
+      p[b] = in ? inv[j0 + b] : -1;
+      w[b] = in && wts ? wts[j0 + b] : 1.f;
     }
 #pragma unroll
     for (int b = 0; b < B; ++b) {
-      if (!on[b]) continue;
+      const bool on = (unsigned)p[b] < (unsigned)P;
+      // a choice left out reads nothing (H = 0) and counts with weight 0 on zeros
+      w[b] = on ? w[b] : 0.f;
+      r[b] = load_raw<VEC>(rows + (int64_t)(on ? p[b] : 0) * ld, c, nt, tid, on ? H : 0);
+    }
+#pragma unroll
+    for (int b = 0; b < B; ++b)
 #pragma unroll
       for (int e = 0; e < 8; ++e) out[e] = fmaf(w[b], RowType<T>::to(r[b].v[e]), out[e]);
-    }
   }
 }
 
