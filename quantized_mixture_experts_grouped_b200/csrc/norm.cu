@@ -157,7 +157,7 @@ struct BackArgs {
 // norm_sums_kernel adds in block order (no atomics: bit-identical run to run).
 template <typename T, bool VEC, int NC, int MAXT>
 __global__ void __launch_bounds__(MAXT) norm_backward_kernel(const BackArgs a) {
-  __shared__ float buf[2][32 * 3];
+  __shared__ float buf[2][32 * 4];
   int flip = 0;                    // the buffer of the next block-wide sums: never the one of the last
   pdl_begin();
   const int nt = blockDim.x, tid = threadIdx.x, H = a.H;
@@ -291,12 +291,19 @@ __device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
 }
 
 template <typename T>
-__device__ __forceinline__ void ring_load(const unsigned char* s, int nt, float (&f)[8]) {
+__device__ __forceinline__ void ring_load(const unsigned char* s, int nt, F2 (&f)[4]) {
   Raw8<T> r;
   uint4* q = reinterpret_cast<uint4*>(&r);
 #pragma unroll
   for (int i = 0; i < (int)sizeof(T) / 2; ++i) q[i] = *reinterpret_cast<const uint4*>(s + (size_t)i * nt * 16);
-  to_float(r, f);
+  to_pairs(r, f);
+}
+
+template <typename T>
+__device__ __forceinline__ void store_pairs(void* base, int64_t ld, int64_t t, int n0, int H, const F2 (&f)[4]) {
+  Raw8<T> r;
+  from_pairs(f, r);
+  store_raw(static_cast<T*>(base) + t * ld, n0, H, r);
 }
 
 constexpr int kRingStages = 4;
@@ -306,7 +313,7 @@ template <typename T, int MAXT>
 __global__ void __launch_bounds__(MAXT, MAXT <= 256 ? 2 : 1) norm_backward_ring_kernel(const BackArgs a, int stages,
                                                                                        int stage_bytes) {
   extern __shared__ __align__(16) unsigned char ring[];
-  __shared__ float buf[2][32 * 3];
+  __shared__ float buf[2][32 * 4];
   int flip = 0;
   constexpr int W = (int)sizeof(T) / 2;              // 16-byte words per thread and tensor
   const int nt = blockDim.x, tid = threadIdx.x, H = a.H, n0 = tid * 8;
@@ -347,9 +354,10 @@ __global__ void __launch_bounds__(MAXT, MAXT <= 256 ? 2 : 1) norm_backward_ring_
   if (a.norm_y && a.w) w = load_raw<true>(static_cast<const T*>(a.w), 0, nt, tid, H);
   if (a.next && a.w_next) wn = load_raw<true>(static_cast<const T*>(a.w_next), 0, nt, tid, H);
   if (a.gate_mode == MOE_GATE_CHANNEL) gc = load_raw<true>(static_cast<const T*>(a.gate), 0, nt, tid, H);
-  float sw[8], sg[8], sn[8];
+  F2 sw[4], sg[4], sn[4];
+  const F2 zero = f2(0.f, 0.f), alpha = f2(a.alpha, a.alpha);
 #pragma unroll
-  for (int e = 0; e < 8; ++e) sw[e] = sg[e] = sn[e] = 0.f;
+  for (int e = 0; e < 4; ++e) sw[e] = sg[e] = sn[e] = zero;
   int stage = 0;
   for (int64_t t = blockIdx.x; t < a.T; t += gridDim.x) {
     issue(t + (int64_t)(stages - 1) * gridDim.x, stage == 0 ? stages - 1 : stage - 1);
@@ -359,22 +367,24 @@ __global__ void __launch_bounds__(MAXT, MAXT <= 256 ? 2 : 1) norm_backward_ring_
     else asm volatile("cp.async.wait_group 1;" ::: "memory");
     const unsigned char* s0 = own + (size_t)stage * stage_bytes;
     stage = stage + 1 == stages ? 0 : stage + 1;
-    float d[8], y[8], h[8], x[8];
-    float s[3] = {0.f, 0.f, 0.f};     // sum h'^2, sum w' dx h', sum y^2
+    F2 d[4], y[4], h[4], x[4], v[4];
+    F2 p0 = zero, p1 = zero, p2 = zero;     // sum h'^2, sum w' dx h', sum y^2
     if (a.next) {
       ring_load<T>(s0 + at_h, nt, h);
       ring_load<T>(s0 + at_x, nt, x);
+      to_pairs(wn, v);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        s[0] = fmaf(h[e], h[e], s[0]);
-        s[1] = fmaf(RowType<T>::to(wn.v[e]) * x[e], h[e], s[1]);
+      for (int e = 0; e < 4; ++e) {
+        p0 = fma2(h[e], h[e], p0);
+        p1 = fma2(mul2(v[e], x[e]), h[e], p1);
       }
     }
     if (a.has_y) ring_load<T>(s0 + at_y, nt, y);
     if (a.norm_y) {
 #pragma unroll
-      for (int e = 0; e < 8; ++e) s[2] = fmaf(y[e], y[e], s[2]);
+      for (int e = 0; e < 4; ++e) p2 = fma2(y[e], y[e], p2);
     }
+    float s[3] = {sum_of(p0), sum_of(p1), sum_of(p2)};
     if (a.next || a.norm_y) {
       block_sums<3>(s, buf[flip]);
       flip ^= 1;
@@ -383,73 +393,80 @@ __global__ void __launch_bounds__(MAXT, MAXT <= 256 ? 2 : 1) norm_backward_ring_
       ring_load<T>(s0, nt, d);
     } else {
 #pragma unroll
-      for (int e = 0; e < 8; ++e) d[e] = 0.f;
+      for (int e = 0; e < 4; ++e) d[e] = zero;
     }
     if (a.next) {
       const float r = rsqrtf(s[0] * inv_h + a.eps);
-      const float m = s[1] * inv_h * r;              // mean(w' dx n), n = h' r
+      const float m = -(s[1] * inv_h * r);           // -mean(w' dx n), n = h' r
+      const F2 r2 = f2(r, r), m2 = f2(m, m);
+      to_pairs(wn, v);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const float n = h[e] * r;
-        d[e] += r * (RowType<T>::to(wn.v[e]) * x[e] - n * m);
-        sn[e] = fmaf(x[e], n, sn[e]);
+      for (int e = 0; e < 4; ++e) {
+        const F2 n = mul2(h[e], r2);
+        d[e] = fma2(r2, fma2(n, m2, mul2(v[e], x[e])), d[e]);
+        sn[e] = fma2(x[e], n, sn[e]);
       }
     }
-    float o[8];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) o[e] = a.alpha * d[e];
-    store8<true>(static_cast<T*>(a.dh) + t * a.lddh, 0, nt, tid, H, o);
+    for (int e = 0; e < 4; ++e) v[e] = mul2(alpha, d[e]);
+    store_pairs<T>(a.dh, a.lddh, t, n0, H, v);
     if (!a.has_y) continue;
     const float q = a.norm_y ? rsqrtf(s[2] * inv_h + a.eps) : 1.f;
-    float z[2] = {0.f, 0.f};          // sum w du n, sum d u
-    float g[8], u[8];
+    const F2 q2 = f2(q, q);
+    F2 g[4], u[4], z0 = zero, z1 = zero;             // sum w du n, sum d u
     if (full) {
       ring_load<T>(s0 + at_g, nt, g);
     } else if (a.gate_mode == MOE_GATE_TOKEN) {
-      const float v = static_cast<const float*>(a.gate)[t];
+      const float k = static_cast<const float*>(a.gate)[t];
 #pragma unroll
-      for (int e = 0; e < 8; ++e) g[e] = v;
+      for (int e = 0; e < 4; ++e) g[e] = f2(k, k);
     } else {
-      to_float(gc, g);
+      to_pairs(gc, g);
     }
+    to_pairs(w, v);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      y[e] *= q;
-      u[e] = d[e] * (y[e] * RowType<T>::to(w.v[e]));   // d u
-      d[e] *= g[e];                                    // du
+    for (int e = 0; e < 4; ++e) {
+      y[e] = mul2(y[e], q2);
+      u[e] = mul2(d[e], mul2(y[e], v[e]));           // d u
+      d[e] = mul2(d[e], g[e]);                       // du
     }
     if (full) {
-      if (a.dgate) store8<true>(static_cast<T*>(a.dgate) + t * a.lddg, 0, nt, tid, H, u);
+      if (a.dgate) store_pairs<T>(a.dgate, a.lddg, t, n0, H, u);
     } else if (a.gate_mode == MOE_GATE_CHANNEL) {
 #pragma unroll
-      for (int e = 0; e < 8; ++e) sg[e] += u[e];
+      for (int e = 0; e < 4; ++e) sg[e] = add2(sg[e], u[e]);
     } else if (a.gate_mode == MOE_GATE_TOKEN) {
 #pragma unroll
-      for (int e = 0; e < 8; ++e) z[1] += u[e];
+      for (int e = 0; e < 4; ++e) z1 = add2(z1, u[e]);
     }
     if (a.norm_y) {
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        sw[e] = fmaf(d[e], y[e], sw[e]);
-        d[e] *= RowType<T>::to(w.v[e]);
-        z[0] = fmaf(d[e], y[e], z[0]);
+      for (int e = 0; e < 4; ++e) {
+        sw[e] = fma2(d[e], y[e], sw[e]);
+        d[e] = mul2(d[e], v[e]);
+        z0 = fma2(d[e], y[e], z0);
       }
     }
+    float z[2] = {sum_of(z0), sum_of(z1)};
     if (a.norm_y || a.gate_mode == MOE_GATE_TOKEN) {
       block_sums<2>(z, buf[flip]);
       flip ^= 1;
     }
     if (a.gate_mode == MOE_GATE_TOKEN && a.dgate && tid == 0) static_cast<float*>(a.dgate)[t] = z[1];
     if (a.norm_y) {
-      const float m = z[0] * inv_h;
+      const float m = -(z[0] * inv_h);
+      const F2 m2 = f2(m, m);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) d[e] = q * (d[e] - y[e] * m);
+      for (int e = 0; e < 4; ++e) d[e] = mul2(q2, fma2(y[e], m2, d[e]));
     }
-    store8<true>(static_cast<T*>(a.dy) + t * a.lddy, 0, nt, tid, H, d);
+    store_pairs<T>(a.dy, a.lddy, t, n0, H, d);
   }
   if (!mine) return;
-  auto leave = [&](float* out, int i, const float(&v)[8]) {
+  auto leave = [&](float* out, int i, const F2(&p)[4]) {
     if (!out) return;
+    Raw8<float> r;
+    from_pairs(p, r);
+    const float(&v)[8] = r.v;
     float4* o = reinterpret_cast<float4*>((gridDim.x == 1 ? out : a.part + ((int64_t)blockIdx.x * kSums + i) * H) + n0);
     if (reinterpret_cast<uintptr_t>(o) & 15) {         // a caller's vector on any boundary
 #pragma unroll

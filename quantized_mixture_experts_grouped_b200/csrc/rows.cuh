@@ -65,17 +65,21 @@ __device__ __forceinline__ void load8(const T* row, int c, int nt, int tid, int 
   to_float(load_raw<VEC>(row, c, nt, tid, H), f);
 }
 
+template <typename T>
+__device__ __forceinline__ void store_raw(T* row, int n0, int H, const Raw8<T>& r) {
+  if (n0 >= H) return;
+  const uint4* q = reinterpret_cast<const uint4*>(&r);
+#pragma unroll
+  for (int i = 0; i < (int)sizeof(T) / 2; ++i) reinterpret_cast<uint4*>(row + n0)[i] = q[i];
+}
+
 template <bool VEC, typename T>
 __device__ __forceinline__ void store8(T* row, int c, int nt, int tid, int H, const float (&f)[8]) {
   Raw8<T> r;
 #pragma unroll
   for (int e = 0; e < 8; ++e) r.v[e] = RowType<T>::from(f[e]);
   if (VEC) {
-    const int n0 = col_of<true>(c, 0, nt, tid);
-    if (n0 >= H) return;
-    const uint4* q = reinterpret_cast<const uint4*>(&r);
-#pragma unroll
-    for (int i = 0; i < (int)sizeof(T) / 2; ++i) reinterpret_cast<uint4*>(row + n0)[i] = q[i];
+    store_raw(row, col_of<true>(c, 0, nt, tid), H, r);
   } else {
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
@@ -85,27 +89,120 @@ __device__ __forceinline__ void store8(T* row, int c, int nt, int tid, int H, co
   }
 }
 
-// N sums over the block, every thread gets them, in an order fixed by the block size. One barrier
-// per call: `buf` (32 * N floats of shared memory) must not be the buffer of the call before.
+// Two fp32 values in one 64-bit register pair: the sm_100 packed forms do both in one instruction.
+// The row kernels with long arithmetic per value are bound by issued instructions, which these halve;
+// each half rounds as the scalar operation does.
+struct F2 {
+  unsigned long long v;
+};
+__device__ __forceinline__ F2 f2(float a, float b) {
+  F2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ float2 halves(F2 p) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(p.v));
+  return r;
+}
+__device__ __forceinline__ float sum_of(F2 p) {
+  const float2 h = halves(p);
+  return h.x + h.y;
+}
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
+  F2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+  return r;
+}
+__device__ __forceinline__ F2 mul2(F2 a, F2 b) {
+  F2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+  return r;
+}
+__device__ __forceinline__ F2 add2(F2 a, F2 b) {
+  F2 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+  return r;
+}
+
+__device__ __forceinline__ void to_pairs(const Raw8<__nv_bfloat16>& r, F2 (&f)[4]) {
+  const uint32_t* w = reinterpret_cast<const uint32_t*>(&r);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) f[i] = f2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u));
+}
+__device__ __forceinline__ void to_pairs(const Raw8<__half>& r, F2 (&f)[4]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) f[i] = f2(__half2float(r.v[2 * i]), __half2float(r.v[2 * i + 1]));
+}
+__device__ __forceinline__ void to_pairs(const Raw8<float>& r, F2 (&f)[4]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) f[i] = f2(r.v[2 * i], r.v[2 * i + 1]);
+}
+__device__ __forceinline__ void from_pairs(const F2 (&f)[4], Raw8<__nv_bfloat16>& r) {
+  __nv_bfloat162* o = reinterpret_cast<__nv_bfloat162*>(&r);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) o[i] = __float22bfloat162_rn(halves(f[i]));
+}
+__device__ __forceinline__ void from_pairs(const F2 (&f)[4], Raw8<__half>& r) {
+  __half2* o = reinterpret_cast<__half2*>(&r);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) o[i] = __float22half2_rn(halves(f[i]));
+}
+__device__ __forceinline__ void from_pairs(const F2 (&f)[4], Raw8<float>& r) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 h = halves(f[i]);
+    r.v[2 * i] = h.x;
+    r.v[2 * i + 1] = h.y;
+  }
+}
+
+// N sums over the block (N = 1, 2, 3, 4 or 8), every thread gets them, in an order fixed by the
+// block size. The lanes of a warp share the values out between them as they add (half of the values
+// to each half-warp, and so on), so 4 sums cost 6 exchanges and not 20. One barrier per call: `buf`
+// (32 * M floats of shared memory) must not be the buffer of the call before.
 template <int N>
 __device__ __forceinline__ void block_sums(float (&v)[N], float* buf) {
+  constexpr int M = N == 3 ? 4 : N;                 // a fourth value, 0, beside three
+  constexpr int L = M == 8 ? 3 : M == 4 ? 2 : M == 2 ? 1 : 0, G = 32 >> L;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nw = blockDim.x >> 5;
+  float x[M];
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1)
+  for (int i = 0; i < M; ++i) x[i] = i < N ? v[i] : 0.f;
 #pragma unroll
-    for (int i = 0; i < N; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], o);
-  if (nw == 1) return;
-  if (lane == 0) {
+  for (int l = 0; l < L; ++l) {
+    const int m = M >> (l + 1), off = 16 >> l;
+    const bool up = lane & off;
 #pragma unroll
-    for (int i = 0; i < N; ++i) buf[i * 32 + warp] = v[i];
+    for (int i = 0; i < m; ++i) {
+      const float keep = up ? x[i + m] : x[i], send = up ? x[i] : x[i + m];
+      x[i] = keep + __shfl_xor_sync(0xffffffffu, send, off);
+    }
   }
-  __syncthreads();
 #pragma unroll
-  for (int i = 0; i < N; ++i) v[i] = lane < nw ? buf[i * 32 + lane] : 0.f;
+  for (int o = G >> 1; o > 0; o >>= 1) x[0] += __shfl_xor_sync(0xffffffffu, x[0], o);
+  if (nw > 1) {     // lane's value: lane / G
+    const int mine = lane & (G - 1);
+    float* row = buf + (lane / G) * 32;
+    if (mine == 0) row[warp] = x[0];
+    __syncthreads();
+    float y[M];
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1)
+    for (int i = 0; i < M; ++i) y[i] = mine + i * G < nw ? row[mine + i * G] : 0.f;
 #pragma unroll
-    for (int i = 0; i < N; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], o);
+    for (int m = M >> 1; m > 0; m >>= 1)
+#pragma unroll
+      for (int i = 0; i < m; ++i) y[i] += y[i + m];
+    x[0] = y[0];
+#pragma unroll
+    for (int o = G >> 1; o > 0; o >>= 1) x[0] += __shfl_xor_sync(0xffffffffu, x[0], o);
+  }
+  if (M == 1) {
+    v[0] = x[0];
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] = __shfl_sync(0xffffffffu, x[0], i * G);
+  }
 }
 
 // out = sum over j of w[j] * rows[inv[j]] (chunk c of a token), in j order; a choice whose inv is
