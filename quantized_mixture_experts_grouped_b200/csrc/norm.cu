@@ -10,14 +10,13 @@
 // All of it moves each row once and does some 10 to 25 flops per value: bound by HBM traffic for
 // large batches, by the latency of one launch for small ones. A block holds one row in registers
 // (8 or 16 values per thread) between its loads and its stores, so no row is read twice.
-#include "rows.cuh"
+#include "norm_back.cuh"
 
 namespace moe {
 
 namespace {
 
 constexpr int kMaxNormH = 16384;
-constexpr int kSums = 3;             // column sums of the backward pass: dw, dgate, dw_next
 
 struct PostArgs {
   const void *y, *h, *w, *gate, *w_next;
@@ -142,21 +141,11 @@ __global__ void __launch_bounds__(1024) norm_post_kernel(const PostArgs a) {
   }
 }
 
-struct BackArgs {
-  const void *dho, *y, *ho, *dx, *w, *gate, *w_next;   // dho may be null (no residual gradient)
-  void *dh, *dy, *dgate;
-  float *dw, *dw_next, *part;      // part: fp32 [blocks][kSums][H], used with more than one block
-  int64_t lddho, ldy, ldho, lddx, ldg, lddh, lddy, lddg;
-  int T, H, gate_mode;
-  bool has_y, norm_y, next;        // has_y false: the gradient of the norm before a block
-  float alpha, eps;
-};
-
 // One block takes rows blockIdx.x, + gridDim.x, ...; every thread keeps the same columns, so the
 // sums over the tokens stay in its registers and leave once per block, as partial sums that
 // norm_sums_kernel adds in block order (no atomics: bit-identical run to run).
 template <typename T, bool VEC, int NC, int MAXT>
-__global__ void __launch_bounds__(MAXT) norm_backward_kernel(const BackArgs a) {
+__global__ void __launch_bounds__(MAXT, MAXT <= 256 ? 2 : 1) norm_backward_kernel(const BackArgs a) {
   __shared__ float buf[2][32 * 4];
   int flip = 0;                    // the buffer of the next block-wide sums: never the one of the last
   pdl_begin();
@@ -278,207 +267,6 @@ __global__ void __launch_bounds__(MAXT) norm_backward_kernel(const BackArgs a) {
       }
     }
   }
-}
-
-// The same gradient for rows of 16-byte words whose tensors fit a ring of stages in shared memory:
-// each thread copies its own words of the next rows (cp.async) while it works on this one, so the
-// loads of several rows stay in flight across the two block-wide sums of a row. A thread only reads
-// words it copied itself: the ring needs no barrier. The weights and the per-channel gate stay in
-// registers. T = 8192, H = 4096, bf16, gate per value, next norm: 234 us with loads at the top of
-// each row, when a row's loads waited for the sums of the row before.
-__device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
-}
-
-template <typename T>
-__device__ __forceinline__ void ring_load(const unsigned char* s, int nt, F2 (&f)[4]) {
-  Raw8<T> r;
-  uint4* q = reinterpret_cast<uint4*>(&r);
-#pragma unroll
-  for (int i = 0; i < (int)sizeof(T) / 2; ++i) q[i] = *reinterpret_cast<const uint4*>(s + (size_t)i * nt * 16);
-  to_pairs(r, f);
-}
-
-template <typename T>
-__device__ __forceinline__ void store_pairs(void* base, int64_t ld, int64_t t, int n0, int H, const F2 (&f)[4]) {
-  Raw8<T> r;
-  from_pairs(f, r);
-  store_raw(static_cast<T*>(base) + t * ld, n0, H, r);
-}
-
-constexpr int kRingStages = 4;
-constexpr int kRingBytes = 224 * 1024 - 4096;        // of an SM's 228 KB, for all its blocks
-
-template <typename T, int MAXT>
-__global__ void __launch_bounds__(MAXT, MAXT <= 256 ? 2 : 1) norm_backward_ring_kernel(const BackArgs a, int stages,
-                                                                                       int stage_bytes) {
-  extern __shared__ __align__(16) unsigned char ring[];
-  __shared__ float buf[2][32 * 4];
-  int flip = 0;
-  constexpr int W = (int)sizeof(T) / 2;              // 16-byte words per thread and tensor
-  const int nt = blockDim.x, tid = threadIdx.x, H = a.H, n0 = tid * 8;
-  const bool mine = n0 < H, full = a.gate_mode == MOE_GATE_FULL;
-  const int region = nt * 16 * W;
-  // where each tensor's words lie in a stage
-  const int at_y = a.dho ? region : 0, at_h = at_y + (a.has_y ? region : 0), at_x = at_h + (a.next ? region : 0),
-            at_g = at_x + (a.next ? region : 0);
-  unsigned char* own = ring + tid * 16;
-  if (!mine)
-    for (int o = 0; o < stages * stage_bytes; o += nt * 16) *reinterpret_cast<uint4*>(own + o) = make_uint4(0, 0, 0, 0);
-  const uint32_t own_s = (uint32_t)__cvta_generic_to_shared(own);
-  auto words = [&](uint32_t dst, const void* base, int64_t ld, int64_t t) {
-    const char* src = reinterpret_cast<const char*>(static_cast<const T*>(base) + t * ld + n0);
-#pragma unroll
-    for (int i = 0; i < W; ++i) copy16(dst + i * nt * 16, src + i * 16);
-  };
-  auto issue = [&](int64_t t, int stage) {
-    if (t < a.T && mine) {
-      const uint32_t d = own_s + stage * stage_bytes;
-      if (a.dho) words(d, a.dho, a.lddho, t);
-      if (a.has_y) words(d + at_y, a.y, a.ldy, t);
-      if (a.next) {
-        words(d + at_h, a.ho, a.ldho, t);
-        words(d + at_x, a.dx, a.lddx, t);
-      }
-      if (full) words(d + at_g, a.gate, a.ldg, t);
-    }
-    asm volatile("cp.async.commit_group;" ::: "memory");
-  };
-  pdl_begin();
-  for (int i = 0; i < stages - 1; ++i) issue((int64_t)blockIdx.x + (int64_t)i * gridDim.x, i);
-  const float inv_h = 1.f / (float)H;
-  // ones where there is no weight (also past H, where everything else is 0)
-  Raw8<T> w, wn, gc;
-#pragma unroll
-  for (int e = 0; e < 8; ++e) w.v[e] = wn.v[e] = gc.v[e] = RowType<T>::from(1.f);
-  if (a.norm_y && a.w) w = load_raw<true>(static_cast<const T*>(a.w), 0, nt, tid, H);
-  if (a.next && a.w_next) wn = load_raw<true>(static_cast<const T*>(a.w_next), 0, nt, tid, H);
-  if (a.gate_mode == MOE_GATE_CHANNEL) gc = load_raw<true>(static_cast<const T*>(a.gate), 0, nt, tid, H);
-  F2 sw[4], sg[4], sn[4];
-  const F2 zero = f2(0.f, 0.f), alpha = f2(a.alpha, a.alpha);
-#pragma unroll
-  for (int e = 0; e < 4; ++e) sw[e] = sg[e] = sn[e] = zero;
-  int stage = 0;
-  for (int64_t t = blockIdx.x; t < a.T; t += gridDim.x) {
-    issue(t + (int64_t)(stages - 1) * gridDim.x, stage == 0 ? stages - 1 : stage - 1);
-    // this row's copies are done when at most the stages - 1 groups after it are under way
-    if (stages == 4) asm volatile("cp.async.wait_group 3;" ::: "memory");
-    else if (stages == 3) asm volatile("cp.async.wait_group 2;" ::: "memory");
-    else asm volatile("cp.async.wait_group 1;" ::: "memory");
-    const unsigned char* s0 = own + (size_t)stage * stage_bytes;
-    stage = stage + 1 == stages ? 0 : stage + 1;
-    F2 d[4], y[4], h[4], x[4], v[4];
-    F2 p0 = zero, p1 = zero, p2 = zero;     // sum h'^2, sum w' dx h', sum y^2
-    if (a.next) {
-      ring_load<T>(s0 + at_h, nt, h);
-      ring_load<T>(s0 + at_x, nt, x);
-      to_pairs(wn, v);
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        p0 = fma2(h[e], h[e], p0);
-        p1 = fma2(mul2(v[e], x[e]), h[e], p1);
-      }
-    }
-    if (a.has_y) ring_load<T>(s0 + at_y, nt, y);
-    if (a.norm_y) {
-#pragma unroll
-      for (int e = 0; e < 4; ++e) p2 = fma2(y[e], y[e], p2);
-    }
-    float s[3] = {sum_of(p0), sum_of(p1), sum_of(p2)};
-    if (a.next || a.norm_y) {
-      block_sums<3>(s, buf[flip]);
-      flip ^= 1;
-    }
-    if (a.dho) {
-      ring_load<T>(s0, nt, d);
-    } else {
-#pragma unroll
-      for (int e = 0; e < 4; ++e) d[e] = zero;
-    }
-    if (a.next) {
-      const float r = rsqrtf(s[0] * inv_h + a.eps);
-      const float m = -(s[1] * inv_h * r);           // -mean(w' dx n), n = h' r
-      const F2 r2 = f2(r, r), m2 = f2(m, m);
-      to_pairs(wn, v);
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const F2 n = mul2(h[e], r2);
-        d[e] = fma2(r2, fma2(n, m2, mul2(v[e], x[e])), d[e]);
-        sn[e] = fma2(x[e], n, sn[e]);
-      }
-    }
-#pragma unroll
-    for (int e = 0; e < 4; ++e) v[e] = mul2(alpha, d[e]);
-    store_pairs<T>(a.dh, a.lddh, t, n0, H, v);
-    if (!a.has_y) continue;
-    const float q = a.norm_y ? rsqrtf(s[2] * inv_h + a.eps) : 1.f;
-    const F2 q2 = f2(q, q);
-    F2 g[4], u[4], z0 = zero, z1 = zero;             // sum w du n, sum d u
-    if (full) {
-      ring_load<T>(s0 + at_g, nt, g);
-    } else if (a.gate_mode == MOE_GATE_TOKEN) {
-      const float k = static_cast<const float*>(a.gate)[t];
-#pragma unroll
-      for (int e = 0; e < 4; ++e) g[e] = f2(k, k);
-    } else {
-      to_pairs(gc, g);
-    }
-    to_pairs(w, v);
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      y[e] = mul2(y[e], q2);
-      u[e] = mul2(d[e], mul2(y[e], v[e]));           // d u
-      d[e] = mul2(d[e], g[e]);                       // du
-    }
-    if (full) {
-      if (a.dgate) store_pairs<T>(a.dgate, a.lddg, t, n0, H, u);
-    } else if (a.gate_mode == MOE_GATE_CHANNEL) {
-#pragma unroll
-      for (int e = 0; e < 4; ++e) sg[e] = add2(sg[e], u[e]);
-    } else if (a.gate_mode == MOE_GATE_TOKEN) {
-#pragma unroll
-      for (int e = 0; e < 4; ++e) z1 = add2(z1, u[e]);
-    }
-    if (a.norm_y) {
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        sw[e] = fma2(d[e], y[e], sw[e]);
-        d[e] = mul2(d[e], v[e]);
-        z0 = fma2(d[e], y[e], z0);
-      }
-    }
-    float z[2] = {sum_of(z0), sum_of(z1)};
-    if (a.norm_y || a.gate_mode == MOE_GATE_TOKEN) {
-      block_sums<2>(z, buf[flip]);
-      flip ^= 1;
-    }
-    if (a.gate_mode == MOE_GATE_TOKEN && a.dgate && tid == 0) static_cast<float*>(a.dgate)[t] = z[1];
-    if (a.norm_y) {
-      const float m = -(z[0] * inv_h);
-      const F2 m2 = f2(m, m);
-#pragma unroll
-      for (int e = 0; e < 4; ++e) d[e] = mul2(q2, fma2(y[e], m2, d[e]));
-    }
-    store_pairs<T>(a.dy, a.lddy, t, n0, H, d);
-  }
-  if (!mine) return;
-  auto leave = [&](float* out, int i, const F2(&p)[4]) {
-    if (!out) return;
-    Raw8<float> r;
-    from_pairs(p, r);
-    const float(&v)[8] = r.v;
-    float4* o = reinterpret_cast<float4*>((gridDim.x == 1 ? out : a.part + ((int64_t)blockIdx.x * kSums + i) * H) + n0);
-    if (reinterpret_cast<uintptr_t>(o) & 15) {         // a caller's vector on any boundary
-#pragma unroll
-      for (int e = 0; e < 8; ++e) reinterpret_cast<float*>(o)[e] = v[e];
-    } else {
-      o[0] = make_float4(v[0], v[1], v[2], v[3]);
-      o[1] = make_float4(v[4], v[5], v[6], v[7]);
-    }
-  };
-  leave(a.dw, 0, sw);
-  leave(a.gate_mode == MOE_GATE_CHANNEL ? static_cast<float*>(a.dgate) : nullptr, 1, sg);
-  leave(a.dw_next, 2, sn);
 }
 
 // Adds the blocks' partial sums: 32 columns by 32 runs of blocks per block, each run in block
@@ -605,12 +393,15 @@ int check_post(const char* me, const PostArgs& a, int T, int H, int dtype, int f
   return MOE_OK;
 }
 
-// The kernel built for a block of this size: the fewer threads, the more registers each has.
+// The kernel built for a block of this size: the fewer threads, the more registers each has. Rows of
+// 16-byte words come here only when they are too wide for the ring.
 template <typename T, bool VEC>
 auto back_kernel(Shape sh) {
   if (sh.nc == 2) return norm_backward_kernel<T, VEC, 2, 1024>;
-  if (sh.nt <= 256) return norm_backward_kernel<T, VEC, 1, 256>;
-  if (sh.nt <= 512) return norm_backward_kernel<T, VEC, 1, 512>;
+  if constexpr (!VEC) {
+    if (sh.nt <= 256) return norm_backward_kernel<T, VEC, 1, 256>;
+    if (sh.nt <= 512) return norm_backward_kernel<T, VEC, 1, 512>;
+  }
   return norm_backward_kernel<T, VEC, 1, 1024>;
 }
 
@@ -625,13 +416,14 @@ int launch_back(const char* me, BackArgs& a, int dtype, bool vec, void* ws, size
     return MOE_OK;
   }
   const Shape sh = shape_of(a.H, 1024);
-  // the ring takes as many stages as fit beside the other block of the SM
+  // the ring takes as many stages as fit beside the SM's other block: two at least, five fp32 tensors
+  // of 512 * 8 values being 80 KB
   const int per_sm = sh.nt <= 256 ? 2 : 1;
   const int tensors = (a.dho ? 1 : 0) + (a.has_y ? 1 : 0) + (a.next ? 2 : 0) + (a.gate_mode == MOE_GATE_FULL ? 1 : 0);
   const int stage_bytes = tensors * sh.nt * 8 * (int)dtype_size(dtype);
   const int fit = kRingBytes / per_sm / stage_bytes;
   const int stages = fit < kRingStages ? fit : kRingStages;
-  const bool use_ring = vec && sh.nc == 1 && stages >= 2;
+  const bool use_ring = vec && sh.nc == 1 && sh.nt <= kRingThreads;
   const int blocks = back_blocks(a.T, per_sm);
   if (any && blocks > 1) {
     const size_t need = norm_ws(a.T, a.H);
@@ -643,15 +435,7 @@ int launch_back(const char* me, BackArgs& a, int dtype, bool vec, void* ws, size
   note_launch();
   int rc = by_type(dtype, [&](auto* p) {
     using T = std::remove_pointer_t<decltype(p)>;
-    if (use_ring) {
-      auto ring = sh.nt <= 256 ? norm_backward_ring_kernel<T, 256>
-                               : sh.nt <= 512 ? norm_backward_ring_kernel<T, 512> : norm_backward_ring_kernel<T, 1024>;
-      const size_t smem = (size_t)stages * stage_bytes;
-      if (int e = check_cuda(cudaFuncSetAttribute(ring, cudaFuncAttributeMaxDynamicSharedMemorySize, kRingBytes), me))
-        return e;
-      return check_cuda(launch_pdl(ring, dim3(blocks), dim3(sh.nt), smem, s, a, stages, stage_bytes),
-                        "norm_backward_ring_kernel");
-    }
+    if (use_ring) return launch_norm_ring<T>(a, blocks, sh.nt, stages, stage_bytes, s);
     auto kern = vec ? back_kernel<T, true>(sh) : back_kernel<T, false>(sh);
     return check_cuda(launch_pdl(kern, dim3(blocks), dim3(sh.nt), 0, s, a), "norm_backward_kernel");
   });

@@ -1,0 +1,27 @@
+// The gradient of the norms around a block for rows of 16-byte words (see norm.cu for the formulas).
+#pragma once
+
+#include "rows.cuh"
+
+namespace moe {
+
+constexpr int kSums = 3;                  // column sums of the backward pass: dw, dgate, dw_next
+constexpr int kRingStages = 4;
+constexpr int kRingBytes = 224 * 1024 - 4096;        // of an SM's 228 KB, for all its blocks
+constexpr int kRingThreads = 512;         // most threads of a block of the ring kernel
+
+struct BackArgs {
+  const void *dho, *y, *ho, *dx, *w, *gate, *w_next;   // dho may be null (no residual gradient)
+  void *dh, *dy, *dgate;
+  float *dw, *dw_next, *part;      // part: fp32 [blocks][kSums][H], used with more than one block
+  int64_t lddho, ldy, ldho, lddx, ldg, lddh, lddy, lddg;
+  int T, H, gate_mode;
+  bool has_y, norm_y, next;        // has_y false: the gradient of the norm before a block
+  float alpha, eps;
+};
+
+// Launches the ring kernel for rows of type T (one file per type, so that they compile side by side).
+template <typename T>
+int launch_norm_ring(const BackArgs& a, int blocks, int nt, int stages, int stage_bytes, cudaStream_t s);
+
+}  // namespace moe

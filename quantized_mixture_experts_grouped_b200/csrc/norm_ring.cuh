@@ -1,0 +1,263 @@
+// The ring form of the norms' gradient and its launch, included by one file per row type.
+#pragma once
+
+#include <atomic>
+
+#include "norm_back.cuh"
+
+namespace moe {
+
+namespace {
+
+// The same gradient for rows of 16-byte words whose tensors fit a ring of stages in shared memory:
+// each thread copies its own words of the next rows (cp.async) while it works on this one, so the
+// loads of several rows stay in flight across the two block-wide sums of a row. A thread only reads
+// words it copied itself: the ring needs no barrier. The weights and the per-channel gate stay in
+// registers. T = 8192, H = 4096, bf16, gate per value, next norm: 234 us with loads at the top of
+// each row, when a row's loads waited for the sums of the row before.
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+
+template <typename T>
+__device__ __forceinline__ void ring_load(const unsigned char* s, int nt, F2 (&f)[4]) {
+  Raw8<T> r;
+  uint4* q = reinterpret_cast<uint4*>(&r);
+#pragma unroll
+  for (int i = 0; i < (int)sizeof(T) / 2; ++i) q[i] = *reinterpret_cast<const uint4*>(s + (size_t)i * nt * 16);
+  to_pairs(r, f);
+}
+
+template <typename T>
+__device__ __forceinline__ void store_pairs(void* base, int64_t ld, int64_t t, int n0, int H, const F2 (&f)[4]) {
+  Raw8<T> r;
+  from_pairs(f, r);
+  store_raw(static_cast<T*>(base) + t * ld, n0, H, r);
+}
+
+template <typename T, int MAXT, bool HAS_Y, bool NORM_Y, bool NEXT, int GATE>
+__global__ void __launch_bounds__(MAXT, MAXT <= 256 ? 2 : 1) norm_backward_ring_kernel(const BackArgs a, int stages,
+                                                                                       int stage_bytes) {
+  extern __shared__ __align__(16) unsigned char ring[];
+  __shared__ float buf[2][32 * 4];
+  int flip = 0;
+  constexpr int W = (int)sizeof(T) / 2;              // 16-byte words per thread and tensor
+  const int nt = blockDim.x, tid = threadIdx.x, H = a.H, n0 = tid * 8;
+  constexpr bool full = GATE == MOE_GATE_FULL;
+  const bool mine = n0 < H, has_d = HAS_Y || a.dho;    // only the norm before a block may have no other gradient
+  const int region = nt * 16 * W;
+  // where each tensor's words lie in a stage
+  const int at_y = has_d ? region : 0, at_h = at_y + (HAS_Y ? region : 0), at_x = at_h + (NEXT ? region : 0),
+            at_g = at_x + (NEXT ? region : 0);
+  unsigned char* own = ring + tid * 16;
+  if (!mine)
+    for (int o = 0; o < stages * stage_bytes; o += nt * 16) *reinterpret_cast<uint4*>(own + o) = make_uint4(0, 0, 0, 0);
+  const uint32_t own_s = (uint32_t)__cvta_generic_to_shared(own);
+  auto words = [&](uint32_t dst, const void* base, int64_t ld, int64_t t) {
+    const char* src = reinterpret_cast<const char*>(static_cast<const T*>(base) + t * ld + n0);
+#pragma unroll
+    for (int i = 0; i < W; ++i) copy16(dst + i * nt * 16, src + i * 16);
+  };
+  auto issue = [&](int64_t t, int stage) {
+    if (t < a.T && mine) {
+      const uint32_t d = own_s + stage * stage_bytes;
+      if (has_d) words(d, a.dho, a.lddho, t);
+      if (HAS_Y) words(d + at_y, a.y, a.ldy, t);
+      if (NEXT) {
+        words(d + at_h, a.ho, a.ldho, t);
+        words(d + at_x, a.dx, a.lddx, t);
+      }
+      if (full) words(d + at_g, a.gate, a.ldg, t);
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+  pdl_begin();
+  for (int i = 0; i < stages - 1; ++i) issue((int64_t)blockIdx.x + (int64_t)i * gridDim.x, i);
+  const float inv_h = 1.f / (float)H;
+  // ones where there is no weight (also past H, where everything else is 0)
+  Raw8<T> w, wn, gc;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) w.v[e] = wn.v[e] = gc.v[e] = RowType<T>::from(1.f);
+  if (NORM_Y && a.w) w = load_raw<true>(static_cast<const T*>(a.w), 0, nt, tid, H);
+  if (NEXT && a.w_next) wn = load_raw<true>(static_cast<const T*>(a.w_next), 0, nt, tid, H);
+  if (GATE == MOE_GATE_CHANNEL) gc = load_raw<true>(static_cast<const T*>(a.gate), 0, nt, tid, H);
+  F2 sw[4], sg[4], sn[4];
+  const F2 zero = f2(0.f, 0.f), alpha = f2(a.alpha, a.alpha);
+#pragma unroll
+  for (int e = 0; e < 4; ++e) sw[e] = sg[e] = sn[e] = zero;
+  int stage = 0;
+  for (int64_t t = blockIdx.x; t < a.T; t += gridDim.x) {
+    issue(t + (int64_t)(stages - 1) * gridDim.x, stage == 0 ? stages - 1 : stage - 1);
+    // this row's copies are done when at most the stages - 1 groups after it are under way
+    if (stages == 4) asm volatile("cp.async.wait_group 3;" ::: "memory");
+    else if (stages == 3) asm volatile("cp.async.wait_group 2;" ::: "memory");
+    else asm volatile("cp.async.wait_group 1;" ::: "memory");
+    const unsigned char* s0 = own + (size_t)stage * stage_bytes;
+    stage = stage + 1 == stages ? 0 : stage + 1;
+    F2 d[4], y[4], h[4], x[4], v[4];
+    F2 p0 = zero, p1 = zero, p2 = zero;     // sum h'^2, sum w' dx h', sum y^2
+    if (NEXT) {
+      ring_load<T>(s0 + at_h, nt, h);
+      ring_load<T>(s0 + at_x, nt, x);
+      to_pairs(wn, v);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        p0 = fma2(h[e], h[e], p0);
+        p1 = fma2(mul2(v[e], x[e]), h[e], p1);
+      }
+    }
+    if (HAS_Y) ring_load<T>(s0 + at_y, nt, y);
+    if (NORM_Y) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) p2 = fma2(y[e], y[e], p2);
+    }
+    float s[3] = {sum_of(p0), sum_of(p1), sum_of(p2)};
+    if (NEXT || NORM_Y) {
+      block_sums<3>(s, buf[flip]);
+      flip ^= 1;
+    }
+    if (has_d) {
+      ring_load<T>(s0, nt, d);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) d[e] = zero;
+    }
+    if (NEXT) {
+      const float r = rsqrtf(s[0] * inv_h + a.eps);
+      const float m = -(s[1] * inv_h * r);           // -mean(w' dx n), n = h' r
+      const F2 r2 = f2(r, r), m2 = f2(m, m);
+      to_pairs(wn, v);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const F2 n = mul2(h[e], r2);
+        d[e] = fma2(r2, fma2(n, m2, mul2(v[e], x[e])), d[e]);
+        sn[e] = fma2(x[e], n, sn[e]);
+      }
+    }
+#pragma unroll
+    for (int e = 0; e < 4; ++e) v[e] = mul2(alpha, d[e]);
+    store_pairs<T>(a.dh, a.lddh, t, n0, H, v);
+    if constexpr (!HAS_Y) continue;
+    const float q = NORM_Y ? rsqrtf(s[2] * inv_h + a.eps) : 1.f;
+    const F2 q2 = f2(q, q);
+    F2 g[4], u[4], z0 = zero, z1 = zero;             // sum w du n, sum d u
+    if (full) {
+      ring_load<T>(s0 + at_g, nt, g);
+    } else if (GATE == MOE_GATE_TOKEN) {
+      const float k = static_cast<const float*>(a.gate)[t];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) g[e] = f2(k, k);
+    } else {
+      to_pairs(gc, g);
+    }
+    to_pairs(w, v);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      y[e] = mul2(y[e], q2);
+      u[e] = mul2(d[e], mul2(y[e], v[e]));           // d u
+      d[e] = mul2(d[e], g[e]);                       // du
+    }
+    if (full) {
+      if (a.dgate) store_pairs<T>(a.dgate, a.lddg, t, n0, H, u);
+    } else if (GATE == MOE_GATE_CHANNEL) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) sg[e] = add2(sg[e], u[e]);
+    } else if (GATE == MOE_GATE_TOKEN) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) z1 = add2(z1, u[e]);
+    }
+    if (NORM_Y) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        sw[e] = fma2(d[e], y[e], sw[e]);
+        d[e] = mul2(d[e], v[e]);
+        z0 = fma2(d[e], y[e], z0);
+      }
+    }
+    float z[2] = {sum_of(z0), sum_of(z1)};
+    if (NORM_Y || GATE == MOE_GATE_TOKEN) {
+      block_sums<2>(z, buf[flip]);
+      flip ^= 1;
+    }
+    if (GATE == MOE_GATE_TOKEN && a.dgate && tid == 0) static_cast<float*>(a.dgate)[t] = z[1];
+    if (NORM_Y) {
+      const float m = -(z[0] * inv_h);
+      const F2 m2 = f2(m, m);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) d[e] = mul2(q2, fma2(y[e], m2, d[e]));
+    }
+    store_pairs<T>(a.dy, a.lddy, t, n0, H, d);
+  }
+  if (!mine) return;
+  auto leave = [&](float* out, int i, const F2(&p)[4]) {
+    if (!out) return;
+    Raw8<float> r;
+    from_pairs(p, r);
+    const float(&v)[8] = r.v;
+    float4* o = reinterpret_cast<float4*>((gridDim.x == 1 ? out : a.part + ((int64_t)blockIdx.x * kSums + i) * H) + n0);
+    if (reinterpret_cast<uintptr_t>(o) & 15) {         // a caller's vector on any boundary
+#pragma unroll
+      for (int e = 0; e < 8; ++e) reinterpret_cast<float*>(o)[e] = v[e];
+    } else {
+      o[0] = make_float4(v[0], v[1], v[2], v[3]);
+      o[1] = make_float4(v[4], v[5], v[6], v[7]);
+    }
+  };
+  leave(a.dw, 0, sw);
+  leave(GATE == MOE_GATE_CHANNEL ? static_cast<float*>(a.dgate) : nullptr, 1, sg);
+  leave(a.dw_next, 2, sn);
+}
+
+// What a call has is a template argument: with the branches taken at run time a thread issued 550
+// instructions per row of 8 values, without them 368 (108.9 against 89.7 us at T = 8192, H = 4096).
+template <typename T, int MAXT, bool HAS_Y, bool NORM_Y, bool NEXT, int GATE>
+int launch_one(const BackArgs& a, int blocks, int nt, int stages, int stage_bytes, cudaStream_t s) {
+  auto kern = norm_backward_ring_kernel<T, MAXT, HAS_Y, NORM_Y, NEXT, GATE>;
+  // the shared-memory limit is a property of the kernel on a device: set on its first launch there
+  static std::atomic<uint64_t> allowed{0};
+  int dev = 0;
+  if (int rc = check_cuda(cudaGetDevice(&dev), "norm_backward_ring_kernel: device")) return rc;
+  const uint64_t bit = dev < 64 ? 1ull << dev : 0;
+  if (!(allowed.load(std::memory_order_relaxed) & bit)) {
+    if (int rc = check_cuda(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kRingBytes),
+                            "norm_backward_ring_kernel: shared memory"))
+      return rc;
+    allowed.fetch_or(bit, std::memory_order_relaxed);
+  }
+  return check_cuda(launch_pdl(kern, dim3(blocks), dim3(nt), (size_t)stages * stage_bytes, s, a, stages, stage_bytes),
+                    "norm_backward_ring_kernel");
+}
+
+template <typename T, int MAXT, bool NORM_Y, bool NEXT>
+int by_gate(const BackArgs& a, int blocks, int nt, int stages, int stage_bytes, cudaStream_t s) {
+  switch (a.gate_mode) {
+    case MOE_GATE_CHANNEL:
+      return launch_one<T, MAXT, true, NORM_Y, NEXT, MOE_GATE_CHANNEL>(a, blocks, nt, stages, stage_bytes, s);
+    case MOE_GATE_TOKEN:
+      return launch_one<T, MAXT, true, NORM_Y, NEXT, MOE_GATE_TOKEN>(a, blocks, nt, stages, stage_bytes, s);
+    case MOE_GATE_FULL:
+      return launch_one<T, MAXT, true, NORM_Y, NEXT, MOE_GATE_FULL>(a, blocks, nt, stages, stage_bytes, s);
+    default:
+      return launch_one<T, MAXT, true, NORM_Y, NEXT, MOE_GATE_NONE>(a, blocks, nt, stages, stage_bytes, s);
+  }
+}
+
+template <typename T, int MAXT>
+int by_flags(const BackArgs& a, int blocks, int nt, int stages, int stage_bytes, cudaStream_t s) {
+  if (!a.has_y) return launch_one<T, MAXT, false, false, true, MOE_GATE_NONE>(a, blocks, nt, stages, stage_bytes, s);
+  if (a.norm_y)
+    return a.next ? by_gate<T, MAXT, true, true>(a, blocks, nt, stages, stage_bytes, s)
+                  : by_gate<T, MAXT, true, false>(a, blocks, nt, stages, stage_bytes, s);
+  return a.next ? by_gate<T, MAXT, false, true>(a, blocks, nt, stages, stage_bytes, s)
+                : by_gate<T, MAXT, false, false>(a, blocks, nt, stages, stage_bytes, s);
+}
+
+}  // namespace
+
+template <typename T>
+int launch_norm_ring(const BackArgs& a, int blocks, int nt, int stages, int stage_bytes, cudaStream_t s) {
+  return nt <= 256 ? by_flags<T, 256>(a, blocks, nt, stages, stage_bytes, s)
+                   : by_flags<T, kRingThreads>(a, blocks, nt, stages, stage_bytes, s);
+}
+
+}  // namespace moe

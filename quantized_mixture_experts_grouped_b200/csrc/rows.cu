@@ -26,6 +26,49 @@ namespace cg = cooperative_groups;
 constexpr int kSortThreads = 1024;
 constexpr int kSortCluster = 8;
 
+// Turns the warps' counts per expert into the counts of the warps before each, and total[e] into
+// their sum: eight neighbouring lanes share an expert, four warps each. All 32 warps call it.
+__device__ __forceinline__ void prefix_warps(int32_t (*wcount)[kMaxExperts], int E, int32_t* total) {
+  for (int i = threadIdx.x; i < (E + 3) / 4 * 32; i += kSortThreads) {
+    const int e = i >> 3, part = i & 7;
+    int c[4], sum = 0;
+#pragma unroll
+    for (int w = 0; w < 4; ++w) {
+      c[w] = e < E ? wcount[part * 4 + w][e] : 0;
+      sum += c[w];
+    }
+    int run = sum;
+#pragma unroll
+    for (int o = 1; o < 8; o <<= 1) {
+      const int v = __shfl_up_sync(0xffffffffu, run, o, 8);
+      if (part >= o) run += v;
+    }
+    if (e < E && part == 7) total[e] = run;
+    run -= sum;
+#pragma unroll
+    for (int w = 0; w < 4; ++w) {
+      if (e < E) wcount[part * 4 + w][e] = run;
+      run += c[w];
+    }
+  }
+}
+
+// Inclusive prefix of v over the block's first kMaxExperts threads (0 from the others); the caller
+// has a barrier between this and the next use of wsum.
+__device__ __forceinline__ int prefix_experts(int v, int32_t* wsum) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int u = __shfl_up_sync(0xffffffffu, v, o);
+    if (lane >= o) v += u;
+  }
+  if (threadIdx.x < kMaxExperts && lane == 31) wsum[warp] = v;
+  __syncthreads();
+  if (threadIdx.x < kMaxExperts)
+    for (int w = 0; w < warp; ++w) v += wsum[w];
+  return v;
+}
+
 // Stable counting sort of the P pairs by expert in ONE launch: a cluster of blocks, each with a
 // contiguous run of pairs, each warp with a contiguous part of the block's run. A warp counts its
 // pairs per expert (warp match, so equal ids cost one add), the block prefixes its warps' counts,
@@ -59,29 +102,7 @@ __global__ void __launch_bounds__(kSortThreads) sort_pairs_kernel(const int32_t*
     __syncwarp();
   }
   __syncthreads();
-  // prefix of the warps' counts per expert: eight neighbouring lanes share an expert, four warps each
-  for (int i = threadIdx.x; i < (E + 3) / 4 * 32; i += kSortThreads) {
-    const int e = i >> 3, part = i & 7;
-    int c[4], sum = 0;
-#pragma unroll
-    for (int w = 0; w < 4; ++w) {
-      c[w] = e < E ? wcount[part * 4 + w][e] : 0;
-      sum += c[w];
-    }
-    int run = sum;
-#pragma unroll
-    for (int o = 1; o < 8; o <<= 1) {
-      const int v = __shfl_up_sync(0xffffffffu, run, o, 8);
-      if (part >= o) run += v;
-    }
-    if (e < E && part == 7) total[e] = run;
-    run -= sum;
-#pragma unroll
-    for (int w = 0; w < 4; ++w) {
-      if (e < E) wcount[part * 4 + w][e] = run;
-      run += c[w];
-    }
-  }
+  prefix_warps(wcount, E, total);
   cluster.sync();
   // each block: pairs of expert e in the blocks before it, and in all of them
   int all = 0, before = 0;
@@ -97,17 +118,8 @@ __global__ void __launch_bounds__(kSortThreads) sort_pairs_kernel(const int32_t*
     }
   }
   cg::cluster_group::arrival_token done = cluster.barrier_arrive();   // the others' counts are read
-  // exclusive prefix over the experts: within a warp, then over the (at most 8) warps that hold one
-  int incl = all;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int v = __shfl_up_sync(0xffffffffu, incl, o);
-    if (lane >= o) incl += v;
-  }
-  if (e0 < kMaxExperts && lane == 31) wsum[warp] = incl;
-  __syncthreads();
+  const int incl = prefix_experts(all, wsum);
   if (e0 < E) {
-    for (int w = 0; w < warp; ++w) incl += wsum[w];
     first[e0] = incl - all + before;
     if (rank == 0) {
       counts[e0] = all;
@@ -187,16 +199,7 @@ __global__ void __launch_bounds__(kRowThreads) dispatch_small_kernel(const U* __
       if (es[p] < E) atomicAdd(&place[es[p]], 1);
     __syncthreads();
     const int e = threadIdx.x;   // 256 threads, at most 256 experts
-    const int c = place[e];
-    int incl = c;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int v = __shfl_up_sync(0xffffffffu, incl, o);
-      if (lane >= o) incl += v;
-    }
-    if (lane == 31) wsum[warp] = incl;
-    __syncthreads();
-    for (int w = 0; w < warp; ++w) incl += wsum[w];
+    const int c = place[e], incl = prefix_experts(c, wsum);
     if (e < E) {
       counts[e] = c;
       offsets[e] = incl - c;
