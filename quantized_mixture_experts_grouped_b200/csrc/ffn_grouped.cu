@@ -2,7 +2,7 @@
 // Counts: ExactMoE for Memory-Efficient W4A16 Inference", Abstract: all selected experts run
 // through fused grouped MoE kernels).
 //
-// Launch sequence: permute (group pairs by expert) -> gather rows -> tile plan -> gate/up GEMM
+// Launch sequence: dispatch (pairs sorted by expert, token rows copied to their places) -> tile plan -> gate/up GEMM
 // with fused silu(g)*u -> down GEMM (fp32 rows per token-expert pair) -> router-weighted combine.
 //
 // Both GEMMs are one persistent tcgen05 kernel (sm_100a). A CTA tile is a PAIR of 128-row
@@ -28,6 +28,7 @@
 #include <cudaTypedefs.h>
 
 #include "common.cuh"
+#include "rows.cuh"
 #include "tc.cuh"
 
 namespace moe {
@@ -698,10 +699,9 @@ int ffn_grouped(const FfnArgs& a, cudaStream_t s) {
   uint16_t* hp = reinterpret_cast<uint16_t*>(a.ws + L.hp);
   int* ctl = reinterpret_cast<int*>(a.ws + L.status);
 
-  if (int rc = launch_permute(a.idx, a.T, a.k, a.E, counts, offsets, perm, inv,
-                              reinterpret_cast<int32_t*>(a.ws + L.perm_scratch), s))
+  if (int rc = launch_dispatch(a.x, a.H, sizeof(uint16_t), a.idx, a.T, a.H, a.E, a.k, counts, offsets, perm, inv, xp,
+                               a.H, s))
     return rc;
-  if (int rc = launch_gather_rows(a.x, perm, Tk, a.k, a.H, xp, s)) return rc;
   const int IB = a.I / kRowBlock, HP = a.H / 256;
   // K split of the down GEMM: two halves when even the fewest token chunks this batch can have
   // give fewer than two rounds of down tiles on the SMs, and K holds at least two groups

@@ -241,6 +241,11 @@ __device__ __forceinline__ void weighted_rows(const T* rows, int64_t ld, const i
 }
 
 // ---- host side ----
+// moe_dispatch without its checks; `size` bytes per value, strides in values (rows.cu). Also the grouped
+// layer path's first step.
+int launch_dispatch(const void* x, int64_t ldx, size_t size, const int32_t* idx, int T, int H, int E, int k,
+                    int32_t* counts, int32_t* offsets, int32_t* perm, int32_t* inv, void* xp, int64_t ldp,
+                    cudaStream_t s);
 inline size_t dtype_size(int dtype) {
   return dtype == MOE_DTYPE_F32 ? 4 : dtype == MOE_DTYPE_BF16 || dtype == MOE_DTYPE_F16 ? 2 : 0;
 }
