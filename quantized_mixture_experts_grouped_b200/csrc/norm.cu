@@ -79,10 +79,11 @@ __global__ void __launch_bounds__(1024) norm_pre_kernel(const T* __restrict__ h,
   }
 }
 
-// YT: type of the rows y comes from; FUSED: y is the combine of its token's rows. h_out may be h:
+// YT: type of the rows y comes from (fused: y is the combine of its token's rows). h_out may be h:
 // a thread reads its values of the row before it writes them, and no other thread reads them.
-template <typename T, typename YT, bool FUSED, bool VEC, int NC>
-__global__ void __launch_bounds__(1024) norm_post_kernel(const PostArgs a) {
+// FUSED: the choices read at a time, 0 for rows that are y itself.
+template <typename T, typename YT, int FUSED, bool VEC, int NC, int MAXT>
+__global__ void __launch_bounds__(MAXT) norm_post_kernel(const PostArgs a) {
   __shared__ float buf[2][32];
   pdl_begin();
   const int64_t t = blockIdx.x;
@@ -93,9 +94,9 @@ __global__ void __launch_bounds__(1024) norm_post_kernel(const PostArgs a) {
   for (int c = 0; c < NC; ++c) load8<VEC>(hrow, c, nt, tid, H, h[c]);
 #pragma unroll
   for (int c = 0; c < NC; ++c) {
-    if (FUSED) {
-      weighted_rows<VEC>(static_cast<const YT*>(a.y), a.ldy, a.inv + t * a.k, a.wts + t * a.k, a.k, a.P, c, nt, tid, H,
-                         y[c]);
+    if constexpr (FUSED > 0) {
+      weighted_rows<FUSED, VEC>(static_cast<const YT*>(a.y), a.ldy, a.inv + t * a.k, a.wts + t * a.k, a.k, a.P, c, nt,
+                                tid, H, y[c]);
       if (a.y_out) store8<VEC>(static_cast<T*>(a.y_out) + t * a.ldyo, c, nt, tid, H, y[c]);
     } else {
       load8<VEC>(static_cast<const YT*>(a.y) + t * a.ldy, c, nt, tid, H, y[c]);
@@ -367,8 +368,13 @@ bool gate16(const void* gate, int mode, int64_t ld, size_t z) {
 template <typename T, typename YT, bool FUSED>
 int launch_post(const PostArgs& a, int rows, bool vec, cudaStream_t s) {
   const Shape sh = shape_of(a.H, 1024);
-  auto kern = sh.nc == 1 ? (vec ? norm_post_kernel<T, YT, FUSED, true, 1> : norm_post_kernel<T, YT, FUSED, false, 1>)
-                         : (vec ? norm_post_kernel<T, YT, FUSED, true, 2> : norm_post_kernel<T, YT, FUSED, false, 2>);
+  // a block of up to 256 threads has the registers for eight choices' words at a time, a larger one
+  // for four
+  constexpr int F8 = FUSED ? 8 : 0, F4 = FUSED ? 4 : 0;
+  auto kern = sh.nc == 2 ? (vec ? norm_post_kernel<T, YT, F4, true, 2, 1024> : norm_post_kernel<T, YT, F4, false, 2, 1024>)
+              : !FUSED || sh.nt > 256
+                  ? (vec ? norm_post_kernel<T, YT, F4, true, 1, 1024> : norm_post_kernel<T, YT, F4, false, 1, 1024>)
+                  : (vec ? norm_post_kernel<T, YT, F8, true, 1, 256> : norm_post_kernel<T, YT, F4, false, 1, 256>);
   note_launch();
   return check_cuda(launch_pdl(kern, dim3(rows), dim3(sh.nt), 0, s, a), "norm_post_kernel");
 }

@@ -13,6 +13,8 @@
 // batch one more. Sums are fp32 in a fixed order; each result is rounded once, to its own type.
 #include <cooperative_groups.h>
 
+#include <type_traits>
+
 #include "rows.cuh"
 
 namespace moe {
@@ -260,7 +262,7 @@ int dispatch_units(const void* x, int64_t ldx, const int32_t* idx, int T, int E,
 
 // ------------------------------------------------------------------------------------- combine
 
-template <typename YT, typename OT, bool VEC>
+template <typename YT, typename OT, bool VEC, int B>
 __global__ void __launch_bounds__(kRowThreads) combine_rows_kernel(const YT* __restrict__ yp, int64_t ldy,
                                                                    const int32_t* __restrict__ inv,
                                                                    const float* __restrict__ wts, int k, int P, int H,
@@ -268,7 +270,7 @@ __global__ void __launch_bounds__(kRowThreads) combine_rows_kernel(const YT* __r
   pdl_begin();
   const int64_t t = blockIdx.x;
   float v[8];
-  weighted_rows<VEC>(yp, ldy, inv + t * k, wts ? wts + t * k : nullptr, k, P, blockIdx.y, blockDim.x, threadIdx.x, H,
+  weighted_rows<B, VEC>(yp, ldy, inv + t * k, wts ? wts + t * k : nullptr, k, P, blockIdx.y, blockDim.x, threadIdx.x, H,
                      v);
   store8<VEC>(out + t * ldo, blockIdx.y, blockDim.x, threadIdx.x, H, v);
 }
@@ -279,7 +281,7 @@ __global__ void __launch_bounds__(kRowThreads) combine_rows_kernel(const YT* __r
 constexpr int kDots = 8;
 
 template <typename YT, typename OT, bool VEC>
-__global__ void __launch_bounds__(kRowThreads) combine_backward_kernel(const OT* __restrict__ dout, int64_t ldo,
+__global__ void __launch_bounds__(kRowThreads, VEC ? 4 : 2) combine_backward_kernel(const OT* __restrict__ dout, int64_t ldo,
                                                                        const YT* __restrict__ yp, int64_t ldy,
                                                                        const int32_t* __restrict__ inv,
                                                                        const float* __restrict__ wts, int k, int P,
@@ -309,23 +311,21 @@ __global__ void __launch_bounds__(kRowThreads) combine_backward_kernel(const OT*
     for (int c = 0; c < chunks; ++c) {
       float d[8];
       load8<VEC>(dout + t * ldo, c, nt, tid, H, d);
-      constexpr int B = sizeof(YT) == 2 ? 8 : 4;
+      // four choices' words at a time and four blocks per SM: T = 2048, k = 8, H = 2048 took 54 us for
+      // the whole gradient with eight and three, 49 with four and five (spills), 44 like this
+      constexpr int B = 4;
 #pragma unroll
       for (int b0 = 0; b0 < kDots; b0 += B) {
         if (j0 + b0 >= k) break;
+        Raw8<YT> r[B];
         if (dwts) {
-          Raw8<YT> r[B];
 #pragma unroll
           for (int b = 0; b < B; ++b) {
             const bool on = pos[b0 + b] >= 0;
             r[b] = load_raw<VEC>(yp + (int64_t)(on ? pos[b0 + b] : 0) * ldy, c, nt, tid, on ? H : 0);
           }
-#pragma unroll
-          for (int b = 0; b < B; ++b)
-#pragma unroll
-            for (int e = 0; e < 8; ++e) dot[b0 + b] = fmaf(d[e], RowType<YT>::to(r[b].v[e]), dot[b0 + b]);
         }
-        if (dyp) {
+        if (dyp) {          // does not wait for yp's rows
 #pragma unroll
           for (int b = 0; b < B; ++b) {
             float g[8];
@@ -334,6 +334,12 @@ __global__ void __launch_bounds__(kRowThreads) combine_backward_kernel(const OT*
             const bool on = pos[b0 + b] >= 0;
             store8<VEC>(dyp + (int64_t)(on ? pos[b0 + b] : 0) * lddy, c, nt, tid, on ? H : 0, g);
           }
+        }
+        if (dwts) {
+#pragma unroll
+          for (int b = 0; b < B; ++b)
+#pragma unroll
+            for (int e = 0; e < 8; ++e) dot[b0 + b] = fmaf(d[e], RowType<YT>::to(r[b].v[e]), dot[b0 + b]);
         }
       }
     }
@@ -350,36 +356,37 @@ __global__ void __launch_bounds__(kRowThreads) combine_backward_kernel(const OT*
 
 constexpr int kRouterWarps = 8;
 
-// One warp per token: lane j holds choice j. The row of E gradients is put together in shared
-// memory (zeros, then the chosen ones; a repeated id adds up in choice order) and written whole.
-template <typename LT>
+// One warp per token: lane j holds choice j. The row of E gradients is put together in shared memory
+// (zeros, then the chosen ones; a repeated id adds up in choice order) and written whole, as 16-byte
+// words with VEC. Several tokens per warp (8 lanes each for k = 8) were no faster at 16384 tokens of
+// 256 experts (5.5 us against 5.1) and slower at 64 (2.3 against 1.7).
+template <typename LT, bool VEC>
 __global__ void __launch_bounds__(32 * kRouterWarps) route_backward_kernel(const int32_t* __restrict__ idx,
                                                                            const float* __restrict__ wts,
                                                                            const float* __restrict__ dwts, int T,
                                                                            int E, int k, LT* __restrict__ dlogits,
                                                                            int64_t ldl) {
-  __shared__ float rows[kRouterWarps][kMaxExperts];
-  pdl_begin();
+  __shared__ __align__(16) float rows[kRouterWarps][kMaxExperts];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  float* row = rows[warp];
+  for (int e = lane; e < E; e += 32) row[e] = 0.f;
+  pdl_begin();
   const int64_t t = (int64_t)blockIdx.x * kRouterWarps + warp;
   if (t >= T) return;
-  float* row = rows[warp];
   const int32_t* it = idx + t * k;
   const float *wt = wts + t * k, *dt = dwts + t * k;
   float mean = 0.f;
   for (int j = lane; j < k; j += 32) mean = fmaf(wt[j], dt[j], mean);
-  for (int e = lane; e < E; e += 32) row[e] = 0.f;
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) mean += __shfl_xor_sync(0xffffffffu, mean, o);
   __syncwarp();
-  for (int j0 = 0; j0 < k; j0 += 32) {
-    const int j = j0 + lane;
+  for (int jb = 0; jb < k; jb += 32) {
+    const int j = jb + lane;
     int e = j < k ? it[j] : -1;
     if ((unsigned)e >= (unsigned)E) e = -1;
     const float g = e >= 0 ? wt[j] * (dt[j] - mean) : 0.f;
     const unsigned same = __match_any_sync(0xffffffffu, e);
-    const unsigned below = same & ((1u << lane) - 1u);
-    const int turn = e >= 0 ? __popc(below) : 0;
+    const int turn = e >= 0 ? __popc(same & ((1u << lane) - 1u)) : 0;
     const int turns = __reduce_max_sync(0xffffffffu, turn);
     for (int i = 0; i <= turns; ++i) {
       if (e >= 0 && turn == i) row[e] += g;
@@ -387,7 +394,19 @@ __global__ void __launch_bounds__(32 * kRouterWarps) route_backward_kernel(const
     }
   }
   LT* out = dlogits + t * ldl;
-  for (int e = lane; e < E; e += 32) out[e] = RowType<LT>::from(row[e]);
+  if (VEC) {
+    for (int e = lane * 8; e < E; e += 256) {
+      float v[8];
+      *reinterpret_cast<float4*>(v) = *reinterpret_cast<const float4*>(row + e);
+      *reinterpret_cast<float4*>(v + 4) = *reinterpret_cast<const float4*>(row + e + 4);
+      Raw8<LT> r;
+#pragma unroll
+      for (int c = 0; c < 8; ++c) r.v[c] = RowType<LT>::from(v[c]);
+      store_raw(out, e, E, r);
+    }
+  } else {
+    for (int e = lane; e < E; e += 32) out[e] = RowType<LT>::from(row[e]);
+  }
 }
 
 // ---- host side ----
@@ -416,7 +435,9 @@ int launch_combine_rows(const void* yp, int64_t ldy, int ydt, const int32_t* inv
   return by_types(ydt, odt, [&](auto* y, auto* o) {
     using YT = std::remove_pointer_t<decltype(y)>;
     using OT = std::remove_pointer_t<decltype(o)>;
-    auto kern = vec ? combine_rows_kernel<YT, OT, true> : combine_rows_kernel<YT, OT, false>;
+    // single values fill the registers with four choices; few choices need no more either
+    auto kern = !vec ? combine_rows_kernel<YT, OT, false, 4>
+                     : k > 4 ? combine_rows_kernel<YT, OT, true, 8> : combine_rows_kernel<YT, OT, true, 4>;
     return check_cuda(launch_pdl(kern, grid, dim3(nt), 0, s, static_cast<const YT*>(yp), ldy, inv, wts, k, T * k, H,
                                  static_cast<OT*>(out), ldo),
                       "combine_rows_kernel");
@@ -548,7 +569,9 @@ MOE_API int moe_route_topk_backward(const int32_t* idx, const float* wts, const 
   note_launch();
   return by_types(dtype, dtype, [&](auto* l, auto*) {
     using LT = std::remove_pointer_t<decltype(l)>;
-    return check_cuda(launch_pdl(route_backward_kernel<LT>, dim3(ceil_div(T, kRouterWarps)), dim3(32 * kRouterWarps), 0,
+    const bool vec = E % 8 == 0 && rows16(dlogits, dlogits_stride, sizeof(LT));
+    auto kern = vec ? route_backward_kernel<LT, true> : route_backward_kernel<LT, false>;
+    return check_cuda(launch_pdl(kern, dim3(ceil_div(T, kRouterWarps)), dim3(32 * kRouterWarps), 0,
                                  reinterpret_cast<cudaStream_t>(stream), idx, wts, dwts, T, E, k,
                                  static_cast<LT*>(dlogits), dlogits_stride),
                       "route_backward_kernel");

@@ -209,11 +209,10 @@ __device__ __forceinline__ void block_sums(float (&v)[N], float* buf) {
 // outside [0, P) adds nothing. The places and weights of a batch of choices are read before the
 // first of their rows, and the rows before the first is used, so that one token waits for memory
 // twice and not twice per choice (2048 tokens, 8 choices, H = 2048: 44 us when each row waited for
-// its own place).
-template <bool VEC, typename T>
+// its own place). B: choices read at a time.
+template <int B, bool VEC, typename T>
 __device__ __forceinline__ void weighted_rows(const T* rows, int64_t ld, const int32_t* inv, const float* wts, int k,
                                               int P, int c, int nt, int tid, int H, float (&out)[8]) {
-  constexpr int B = sizeof(T) == 2 ? 8 : 4;   // choices in flight: 128 bytes per thread
 #pragma unroll
   for (int e = 0; e < 8; ++e) out[e] = 0.f;
   for (int j0 = 0; j0 < k; j0 += B) {
