@@ -257,7 +257,7 @@ __global__ void __launch_bounds__(MAXT, MAXT <= 256 ? 2 : 1) norm_backward_kerne
 #pragma unroll
   for (int i = 0; i < kSums; ++i) {
     if (!out[i]) continue;
-    float* o = gridDim.x == 1 ? out[i] : a.part + ((int64_t)blockIdx.x * kSums + i) * H;
+    float* o = gridDim.x == 1 ? out[i] : a.part + ((int64_t)blockIdx.x * kSums + i) * a.part_ld;
 #pragma unroll
     for (int c = 0; c < NC; ++c) {
       const float(&v)[8] = i == 0 ? sw[c] : i == 1 ? sg[c] : sn[c];
@@ -270,30 +270,42 @@ __global__ void __launch_bounds__(MAXT, MAXT <= 256 ? 2 : 1) norm_backward_kerne
   }
 }
 
-// Adds the blocks' partial sums: 32 columns by 32 runs of blocks per block, each run in block
-// order, then the runs in order.
-__global__ void __launch_bounds__(1024) norm_sums_kernel(const float* __restrict__ part, int blocks, int H, float* o0,
-                                                         float* o1, float* o2) {
+// Adds the blocks' partial sums: a block has 32 columns (8 lanes of 16 bytes) by 128 runs, run i
+// taking the blocks i, i + 128, ... in order; then the runs are added in a fixed tree. With 19 blocks
+// after one another per run and single values the sums of 592 blocks took 4.5 us.
+__global__ void __launch_bounds__(1024) norm_sums_kernel(const float* __restrict__ part, int blocks, int H, int ld,
+                                                         float* o0, float* o1, float* o2) {
   __shared__ float sum[32][33];
   pdl_begin();
   float* out = blockIdx.y == 0 ? o0 : blockIdx.y == 1 ? o1 : o2;
   if (!out) return;
-  const int lane = threadIdx.x & 31, run = threadIdx.x >> 5;
-  const int n = blockIdx.x * 32 + lane, per = (blocks + 31) / 32;
-  float v = 0.f;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, run = threadIdx.x >> 3;
+  const int n = blockIdx.x * 32 + (lane & 7) * 4;
+  float v[4] = {0.f, 0.f, 0.f, 0.f};
   if (n < H) {
-    const int b1 = min((run + 1) * per, blocks);
-#pragma unroll 4
-    for (int b = run * per; b < b1; ++b) v += part[((int64_t)b * kSums + blockIdx.y) * H + n];
+    const float* p = part + (int64_t)blockIdx.y * ld + n;
+#pragma unroll 5
+    for (int b = run; b < blocks; b += 128) {
+      const float4 x = *reinterpret_cast<const float4*>(p + (int64_t)b * kSums * ld);
+      v[0] += x.x;
+      v[1] += x.y;
+      v[2] += x.z;
+      v[3] += x.w;
+    }
   }
-  sum[run][lane] = v;
-  __syncthreads();
-  if (run == 0 && n < H) {
-    float total = 0.f;
 #pragma unroll
-    for (int i = 0; i < 32; ++i) total += sum[i][lane];
-    out[n] = total;
+  for (int i = 0; i < 4; ++i) {
+    v[i] += __shfl_xor_sync(0xffffffffu, v[i], 8);
+    v[i] += __shfl_xor_sync(0xffffffffu, v[i], 16);
+    if (lane < 8) sum[warp][lane * 4 + i] = v[i];
   }
+  __syncthreads();
+  // warp w adds column w of the 32 warps
+  float total = sum[lane][warp];
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
+  const int col = blockIdx.x * 32 + warp;
+  if (lane == 0 && col < H) out[col] = total;
 }
 
 // ---- host side ----
@@ -326,16 +338,17 @@ int norm_sms() {
   return n;
 }
 
-// Blocks of the backward kernel never exceed this, so that the workspace's size does not depend on
-// the device.
-constexpr int kMaxBlocks = 592;
-int back_blocks(int T, int per_sm) {
-  const int b = norm_sms() * per_sm;
-  return T < b ? T : b < kMaxBlocks ? b : kMaxBlocks;
+// Blocks of the backward kernel: what the SMs hold at a time, and no more than these, so that the
+// workspace's size does not depend on the device.
+int most_blocks(int H) { return 148 * ring_blocks(row_threads(H, 1024), false); }
+int back_blocks(int T, int H, int per_sm) {
+  const int b = norm_sms() * per_sm, most = most_blocks(H);
+  return T < b ? T : b < most ? b : most;
 }
+int part_stride(int H) { return (H + 3) / 4 * 4; }
 size_t norm_ws(int T, int H) {
-  const size_t b = T < kMaxBlocks ? (T > 0 ? T : 1) : kMaxBlocks;
-  return align_up(b * kSums * (size_t)H * sizeof(float), 256);
+  const size_t most = most_blocks(H), b = (size_t)T < most ? (T > 0 ? T : 1) : most;
+  return align_up(b * kSums * part_stride(H) * sizeof(float), 256);
 }
 
 int check_norm(const char* me, int T, int H, int dtype, float eps) {
@@ -422,15 +435,18 @@ int launch_back(const char* me, BackArgs& a, int dtype, bool vec, void* ws, size
     return MOE_OK;
   }
   const Shape sh = shape_of(a.H, 1024);
-  // the ring takes as many stages as fit beside the SM's other block: two at least, five fp32 tensors
-  // of 512 * 8 values being 80 KB
-  const int per_sm = sh.nt <= 256 ? 2 : 1;
+  // the ring wants three stages (two rows ahead) and takes up to four; fewer blocks share an SM where
+  // that needs their shared memory. Two always fit: five fp32 tensors of 512 * 8 values are 80 KB.
   const int tensors = (a.dho ? 1 : 0) + (a.has_y ? 1 : 0) + (a.next ? 2 : 0) + (a.gate_mode == MOE_GATE_FULL ? 1 : 0);
   const int stage_bytes = tensors * sh.nt * 8 * (int)dtype_size(dtype);
+  int per_sm = ring_blocks(sh.nt, a.has_y);
+  while (per_sm > 1 && kRingBytes / per_sm / stage_bytes < 3) per_sm /= 2;
+  if (per_sm < 1) per_sm = 1;
   const int fit = kRingBytes / per_sm / stage_bytes;
   const int stages = fit < kRingStages ? fit : kRingStages;
-  const bool use_ring = vec && sh.nc == 1 && sh.nt <= kRingThreads;
-  const int blocks = back_blocks(a.T, per_sm);
+  const bool use_ring = vec && sh.nc == 1 && sh.nt <= kRingThreads && stages >= 2;
+  const int blocks = back_blocks(a.T, a.H, per_sm);
+  a.part_ld = part_stride(a.H);
   if (any && blocks > 1) {
     const size_t need = norm_ws(a.T, a.H);
     if (!ws || ws_bytes < need)
@@ -448,7 +464,7 @@ int launch_back(const char* me, BackArgs& a, int dtype, bool vec, void* ws, size
   if (rc || !any || blocks == 1) return rc;
   note_launch();
   return check_cuda(launch_pdl(norm_sums_kernel, dim3(ceil_div(a.H, 32), kSums), dim3(1024), 0, s,
-                               (const float*)a.part, blocks, a.H, sums[0], sums[1], sums[2]),
+                               (const float*)a.part, blocks, a.H, a.part_ld, sums[0], sums[1], sums[2]),
                     "norm_sums_kernel");
 }
 

@@ -13,12 +13,18 @@ constexpr int kRingThreads = 512;         // most threads of a block of the ring
 struct BackArgs {
   const void *dho, *y, *ho, *dx, *w, *gate, *w_next;   // dho may be null (no residual gradient)
   void *dh, *dy, *dgate;
-  float *dw, *dw_next, *part;      // part: fp32 [blocks][kSums][H], used with more than one block
+  float *dw, *dw_next, *part;      // part: fp32 [blocks][kSums][part_ld], used with more than one block
   int64_t lddho, ldy, ldho, lddx, ldg, lddh, lddy, lddg;
-  int T, H, gate_mode;
+  int T, H, part_ld, gate_mode;
   bool has_y, norm_y, next;        // has_y false: the gradient of the norm before a block
   float alpha, eps;
 };
+
+// Blocks of the ring kernel that share an SM by their registers (64 a thread before a block, 128 after
+// one), 16 at most.
+constexpr int ring_blocks(int threads, bool has_y) {
+  return (has_y ? 512 : 1024) / threads < 16 ? (has_y ? 512 : 1024) / threads : 16;
+}
 
 // Launches the ring kernel for rows of type T (one file per type, so that they compile side by side).
 template <typename T>

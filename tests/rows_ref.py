@@ -148,8 +148,8 @@ BACK = 3 * R + ROW_SUM + 6
 
 
 def column_chain(T):
-    """Longest chain of a sum over the tokens: a block's rows, its run of blocks, the 32 runs. The
-    backward pass has between min(T, 100) and 592 blocks."""
+    """Longest chain of a sum over the tokens: a block's rows, its run of at most 19 blocks of 2368, the
+    joining of the runs. The backward pass has at least min(T, 100) blocks."""
     return -(-T // min(T, 100)) + 19 + 32
 
 

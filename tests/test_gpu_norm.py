@@ -40,7 +40,11 @@ def ws_for(T, H):
 WIDTHS = [(1, 1), (3, 7), (2, 2048), (5, 1031), (4, 4096), (3, 8192), (2, 12288 + 256), (2, 16384), (1, 9001)]
 
 
-@pytest.mark.parametrize("T,H", WIDTHS + [(700, 264)])
+# more tokens than blocks at each width, so that a block takes several rows
+LONG = [(5000, 264), (3000, 512), (2500, 72), (1300, 2048), (700, 4096), (500, 8192)]
+
+
+@pytest.mark.parametrize("T,H", WIDTHS + [(700, 264)] + LONG)
 @pytest.mark.parametrize("dt", ["bf16", "f16", "f32"])
 @pytest.mark.parametrize("pad", [0, 8, 1])
 def test_pre(T, H, dt, pad):
@@ -124,7 +128,7 @@ def test_post(norm_y, gate, nxt, dt, T, H, pad):
     assert torch.equal(h, ho)
 
 
-@pytest.mark.parametrize("T,H", WIDTHS + [(700, 264), (1300, 72)])
+@pytest.mark.parametrize("T,H", WIDTHS + [(700, 264), (1300, 72)] + LONG)
 @pytest.mark.parametrize("dt", ["bf16", "f32"])
 def test_post_widths(T, H, dt):
     """Every block size, more tokens than blocks (partial sums), no weights (ones)."""
