@@ -8,8 +8,10 @@
 //   Gradient of rms(v) w towards v, applied to d, with n = rms(v):  r (w d - n mean(w d n)).
 //
 // All of it moves each row once and does some 10 to 25 flops per value: bound by HBM traffic for
-// large batches, by the latency of one launch for small ones. A block holds one row in registers
+// large batches, by the latency of one launch for small ones. A block holds its rows in registers
 // (8 or 16 values per thread) between its loads and its stores, so no row is read twice.
+#include <type_traits>
+
 #include "norm_back.cuh"
 
 namespace moe {
@@ -24,58 +26,72 @@ struct PostArgs {
   int64_t ldy, ldh, ldg, ldho, ldx, ldyo;
   const int32_t* inv;                // fused combine: y = sum_j wts * yp[inv]
   const float* wts;
-  int k, P, H, gate_mode;
+  int k, P, T, H, gate_mode;
   bool norm_y, next;
   float alpha, eps;
 };
 
 // The value of one weight or gate vector at this thread's columns (ones where there is none).
 template <bool VEC, typename T>
-__device__ __forceinline__ void weight8(const void* w, int c, int nt, int tid, int H, float (&f)[8]) {
+__device__ __forceinline__ void weight8(const void* w, int c, int nt, int tid, int H, F2 (&f)[4]) {
   if (w) {
     load8<VEC>(static_cast<const T*>(w), c, nt, tid, H, f);
   } else {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) f[e] = 1.f;
+    for (int e = 0; e < 4; ++e) f[e] = f2(1.f, 1.f);
   }
 }
 
 // The gate of token t at this thread's columns.
 template <bool VEC, typename T>
 __device__ __forceinline__ void gate8(const void* g, int mode, int64_t ld, int64_t t, int c, int nt, int tid, int H,
-                                      float (&f)[8]) {
+                                      F2 (&f)[4]) {
   if (mode == MOE_GATE_CHANNEL || mode == MOE_GATE_FULL) {
     load8<VEC>(static_cast<const T*>(g) + (mode == MOE_GATE_FULL ? t * ld : 0), c, nt, tid, H, f);
   } else {
     const float v = mode == MOE_GATE_TOKEN ? static_cast<const float*>(g)[t] : 1.f;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) f[e] = v;
+    for (int e = 0; e < 4; ++e) f[e] = f2(v, v);
   }
 }
 
-template <typename T, bool VEC, int NC>
-__global__ void __launch_bounds__(1024) norm_pre_kernel(const T* __restrict__ h, int64_t ldh, const T* __restrict__ w,
-                                                        float eps, int H, T* __restrict__ x, int64_t ldx) {
-  __shared__ float buf[32];
-  pdl_begin();
-  const int64_t t = blockIdx.x;
-  const int nt = blockDim.x, tid = threadIdx.x;
-  float v[NC][8], wv[NC][8], ss[1] = {0.f};
-#pragma unroll
-  for (int c = 0; c < NC; ++c) load8<VEC>(h + t * ldh, c, nt, tid, H, v[c]);
-#pragma unroll
-  for (int c = 0; c < NC; ++c) weight8<VEC, T>(w, c, nt, tid, H, wv[c]);
+// The sum of the squares of a thread's values.
+template <int NC>
+__device__ __forceinline__ float squares(const F2 (&v)[NC][4]) {
+  F2 s = f2(0.f, 0.f);
 #pragma unroll
   for (int c = 0; c < NC; ++c)
 #pragma unroll
-    for (int e = 0; e < 8; ++e) ss[0] = fmaf(v[c][e], v[c][e], ss[0]);
-  block_sums<1>(ss, buf);
+    for (int e = 0; e < 4; ++e) s = fma2(v[c][e], v[c][e], s);
+  return sum_of(s);
+}
+
+// A block of the forward kernels has blockDim.y rows of blockDim.x threads: narrow rows share a block,
+// so that it has 256 threads (8192 rows of 512 values took 8.9 us with a block each). Rows past the
+// last read as zeros and write nothing.
+constexpr int kBlockRows = 8;
+
+template <typename T, bool VEC, int NC, int MAXT>
+__global__ void __launch_bounds__(MAXT) norm_pre_kernel(const T* __restrict__ h, int64_t ldh, const T* __restrict__ w,
+                                                        float eps, int rows, int H, T* __restrict__ x, int64_t ldx) {
+  __shared__ float buf[kBlockRows][32];
+  pdl_begin();
+  const int64_t t = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
+  const int nt = blockDim.x, tid = threadIdx.x, live = t < rows ? H : 0;
+  F2 v[NC][4], w8[NC][4];
+#pragma unroll
+  for (int c = 0; c < NC; ++c) load8<VEC>(h + t * ldh, c, nt, tid, live, v[c]);
+#pragma unroll
+  for (int c = 0; c < NC; ++c) weight8<VEC, T>(w, c, nt, tid, H, w8[c]);
+  float ss[1] = {squares(v)};
+  block_sums<1>(ss, buf[threadIdx.y]);
   const float r = rsqrtf(ss[0] / H + eps);
+  const F2 r2 = f2(r, r);
 #pragma unroll
   for (int c = 0; c < NC; ++c) {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) v[c][e] = v[c][e] * r * wv[c][e];
-    store8<VEC>(x + t * ldx, c, nt, tid, H, v[c]);
+    for (int e = 0; e < 4; ++e) v[c][e] = mul2(mul2(v[c][e], r2), w8[c][e]);
+    store8<VEC>(x + t * ldx, c, nt, tid, live, v[c]);
   }
 }
 
@@ -83,62 +99,58 @@ __global__ void __launch_bounds__(1024) norm_pre_kernel(const T* __restrict__ h,
 // a thread reads its values of the row before it writes them, and no other thread reads them.
 // FUSED: the choices read at a time, 0 for rows that are y itself.
 template <typename T, typename YT, int FUSED, bool VEC, int NC, int MAXT>
-__global__ void __launch_bounds__(MAXT) norm_post_kernel(const PostArgs a) {
-  __shared__ float buf[2][32];
+__global__ void __launch_bounds__(MAXT, MAXT == 256 && VEC && !FUSED && NC == 1 ? 8 : 1) norm_post_kernel(const PostArgs a) {
+  __shared__ float buf[2][kBlockRows][32];
   pdl_begin();
-  const int64_t t = blockIdx.x;
-  const int nt = blockDim.x, tid = threadIdx.x, H = a.H;
-  float h[NC][8], y[NC][8], s[1] = {0.f};
+  const int64_t t = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
+  const int nt = blockDim.x, tid = threadIdx.x, H = a.H, live = t < a.T ? H : 0;
+  F2 h[NC][4], y[NC][4], f[4];
+  float s[1];
   const T* hrow = static_cast<const T*>(a.h) + t * a.ldh;
 #pragma unroll
-  for (int c = 0; c < NC; ++c) load8<VEC>(hrow, c, nt, tid, H, h[c]);
+  for (int c = 0; c < NC; ++c) load8<VEC>(hrow, c, nt, tid, live, h[c]);
+  if constexpr (FUSED > 0) {
+    weighted_rows<FUSED, NC, VEC>(static_cast<const YT*>(a.y), a.ldy, a.inv + t * a.k, a.wts + t * a.k, live ? a.k : 0,
+                                  a.P, 0, nt, tid, H, y);
+    if (a.y_out) {
 #pragma unroll
-  for (int c = 0; c < NC; ++c) {
-    if constexpr (FUSED > 0) {
-      weighted_rows<FUSED, VEC>(static_cast<const YT*>(a.y), a.ldy, a.inv + t * a.k, a.wts + t * a.k, a.k, a.P, c, nt,
-                                tid, H, y[c]);
-      if (a.y_out) store8<VEC>(static_cast<T*>(a.y_out) + t * a.ldyo, c, nt, tid, H, y[c]);
-    } else {
-      load8<VEC>(static_cast<const YT*>(a.y) + t * a.ldy, c, nt, tid, H, y[c]);
+      for (int c = 0; c < NC; ++c) store8<VEC>(static_cast<T*>(a.y_out) + t * a.ldyo, c, nt, tid, live, y[c]);
     }
+  } else {
+#pragma unroll
+    for (int c = 0; c < NC; ++c) load8<VEC>(static_cast<const YT*>(a.y) + t * a.ldy, c, nt, tid, live, y[c]);
   }
   if (a.norm_y) {
-#pragma unroll
-    for (int c = 0; c < NC; ++c)
-#pragma unroll
-      for (int e = 0; e < 8; ++e) s[0] = fmaf(y[c][e], y[c][e], s[0]);
-    block_sums<1>(s, buf[0]);
+    s[0] = squares(y);
+    block_sums<1>(s, buf[0][threadIdx.y]);
     const float q = rsqrtf(s[0] / H + a.eps);
+    const F2 q2 = f2(q, q);
 #pragma unroll
     for (int c = 0; c < NC; ++c) {
-      float w[8];
-      weight8<VEC, T>(a.w, c, nt, tid, H, w);
+      weight8<VEC, T>(a.w, c, nt, tid, H, f);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) y[c][e] = y[c][e] * q * w[e];
+      for (int e = 0; e < 4; ++e) y[c][e] = mul2(mul2(y[c][e], q2), f[e]);
     }
   }
-  s[0] = 0.f;
+  const F2 alpha = f2(a.alpha, a.alpha);
 #pragma unroll
   for (int c = 0; c < NC; ++c) {
-    float g[8];
-    gate8<VEC, T>(a.gate, a.gate_mode, a.ldg, t, c, nt, tid, H, g);
+    gate8<VEC, T>(a.gate, a.gate_mode, a.ldg, live ? t : 0, c, nt, tid, H, f);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      h[c][e] = fmaf(a.alpha, h[c][e], g[e] * y[c][e]);
-      s[0] = fmaf(h[c][e], h[c][e], s[0]);
-    }
-    store8<VEC>(static_cast<T*>(a.h_out) + t * a.ldho, c, nt, tid, H, h[c]);
+    for (int e = 0; e < 4; ++e) h[c][e] = fma2(alpha, h[c][e], mul2(f[e], y[c][e]));
+    store8<VEC>(static_cast<T*>(a.h_out) + t * a.ldho, c, nt, tid, live, h[c]);
   }
   if (!a.next) return;
-  block_sums<1>(s, buf[1]);
+  s[0] = squares(h);
+  block_sums<1>(s, buf[1][threadIdx.y]);
   const float r = rsqrtf(s[0] / H + a.eps);
+  const F2 r2 = f2(r, r);
 #pragma unroll
   for (int c = 0; c < NC; ++c) {
-    float w[8];
-    weight8<VEC, T>(a.w_next, c, nt, tid, H, w);
+    weight8<VEC, T>(a.w_next, c, nt, tid, H, f);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) h[c][e] = h[c][e] * r * w[e];
-    store8<VEC>(static_cast<T*>(a.x_next) + t * a.ldx, c, nt, tid, H, h[c]);
+    for (int e = 0; e < 4; ++e) h[c][e] = mul2(mul2(h[c][e], r2), f[e]);
+    store8<VEC>(static_cast<T*>(a.x_next) + t * a.ldx, c, nt, tid, live, h[c]);
   }
 }
 
@@ -152,16 +164,19 @@ __global__ void __launch_bounds__(MAXT, MAXT <= 256 ? 2 : 1) norm_backward_kerne
   pdl_begin();
   const int nt = blockDim.x, tid = threadIdx.x, H = a.H;
   const float inv_h = 1.f / (float)H;
-  float sw[NC][8], sg[NC][8], sn[NC][8];
+  const F2 zero = f2(0.f, 0.f), alpha = f2(a.alpha, a.alpha);
+  F2 sw[NC][4], sg[NC][4], sn[NC][4];
 #pragma unroll
   for (int c = 0; c < NC; ++c)
 #pragma unroll
-    for (int e = 0; e < 8; ++e) sw[c][e] = sg[c][e] = sn[c][e] = 0.f;
+    for (int e = 0; e < 4; ++e) sw[c][e] = sg[c][e] = sn[c][e] = zero;
   for (int64_t t = blockIdx.x; t < a.T; t += gridDim.x) {
-    float d[NC][8], y[NC][8], h[NC][8], x[NC][8];
-    float s[3] = {0.f, 0.f, 0.f};     // sum h'^2, sum w' dx h', sum y^2
+    F2 d[NC][4], y[NC][4], h[NC][4], x[NC][4], f[4];
+    F2 p0 = zero, p1 = zero, p2 = zero;     // sum h'^2, sum w' dx h', sum y^2
 #pragma unroll
     for (int c = 0; c < NC; ++c) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) d[c][e] = zero;
       if (a.dho) load8<VEC>(static_cast<const T*>(a.dho) + t * a.lddho, c, nt, tid, H, d[c]);
       if (a.has_y) load8<VEC>(static_cast<const T*>(a.y) + t * a.ldy, c, nt, tid, H, y[c]);
       if (a.next) {
@@ -171,85 +186,83 @@ __global__ void __launch_bounds__(MAXT, MAXT <= 256 ? 2 : 1) norm_backward_kerne
     }
 #pragma unroll
     for (int c = 0; c < NC; ++c) {
-      if (!a.dho) {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) d[c][e] = 0.f;
-      }
       if (a.next) {
-        float w[8];
-        weight8<VEC, T>(a.w_next, c, nt, tid, H, w);
+        weight8<VEC, T>(a.w_next, c, nt, tid, H, f);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          s[0] = fmaf(h[c][e], h[c][e], s[0]);
-          s[1] = fmaf(w[e] * x[c][e], h[c][e], s[1]);
+        for (int e = 0; e < 4; ++e) {
+          p0 = fma2(h[c][e], h[c][e], p0);
+          p1 = fma2(mul2(f[e], x[c][e]), h[c][e], p1);
         }
       }
       if (a.norm_y) {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) s[2] = fmaf(y[c][e], y[c][e], s[2]);
+        for (int e = 0; e < 4; ++e) p2 = fma2(y[c][e], y[c][e], p2);
       }
     }
+    float s[3] = {sum_of(p0), sum_of(p1), sum_of(p2)};
     if (a.next || a.norm_y) {
       block_sums<3>(s, buf[flip]);
       flip ^= 1;
     }
     if (a.next) {
       const float r = rsqrtf(s[0] * inv_h + a.eps);
-      const float m = s[1] * inv_h * r;              // mean(w' dx n), n = h' r
+      const float m = -(s[1] * inv_h * r);           // -mean(w' dx n), n = h' r
+      const F2 r2 = f2(r, r), m2 = f2(m, m);
 #pragma unroll
       for (int c = 0; c < NC; ++c) {
-        float w[8];
-        weight8<VEC, T>(a.w_next, c, nt, tid, H, w);
+        weight8<VEC, T>(a.w_next, c, nt, tid, H, f);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const float n = h[c][e] * r;
-          d[c][e] += r * (w[e] * x[c][e] - n * m);
-          sn[c][e] = fmaf(x[c][e], n, sn[c][e]);
+        for (int e = 0; e < 4; ++e) {
+          const F2 n = mul2(h[c][e], r2);
+          d[c][e] = fma2(r2, fma2(n, m2, mul2(f[e], x[c][e])), d[c][e]);
+          sn[c][e] = fma2(x[c][e], n, sn[c][e]);
         }
       }
     }
     // dh = alpha d
 #pragma unroll
     for (int c = 0; c < NC; ++c) {
-      float o[8];
 #pragma unroll
-      for (int e = 0; e < 8; ++e) o[e] = a.alpha * d[c][e];
-      store8<VEC>(static_cast<T*>(a.dh) + t * a.lddh, c, nt, tid, H, o);
+      for (int e = 0; e < 4; ++e) f[e] = mul2(alpha, d[c][e]);
+      store8<VEC>(static_cast<T*>(a.dh) + t * a.lddh, c, nt, tid, H, f);
     }
     if (!a.has_y) continue;
     const float q = a.norm_y ? rsqrtf(s[2] * inv_h + a.eps) : 1.f;
-    float z[2] = {0.f, 0.f};          // sum w du n, sum d u
+    const F2 q2 = f2(q, q);
+    F2 z0 = zero, z1 = zero;                         // sum w du n, sum d u
 #pragma unroll
     for (int c = 0; c < NC; ++c) {
-      float w[8], g[8];
-      if (a.norm_y) weight8<VEC, T>(a.w, c, nt, tid, H, w);
+      F2 g[4], u[4];
+      weight8<VEC, T>(a.norm_y ? a.w : nullptr, c, nt, tid, H, f);
       gate8<VEC, T>(a.gate, a.gate_mode, a.ldg, t, c, nt, tid, H, g);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const float n = y[c][e] * q, we = a.norm_y ? w[e] : 1.f;
-        const float du = g[e] * d[c][e];
-        const float dg = d[c][e] * n * we;           // d u
-        z[1] += dg;
-        if (a.gate_mode == MOE_GATE_CHANNEL) sg[c][e] += dg;
-        if (a.norm_y) sw[c][e] = fmaf(du, n, sw[c][e]);
-        z[0] = fmaf(we * du, n, z[0]);
-        g[e] = dg;
-        d[c][e] = we * du;
-        y[c][e] = n;
+      for (int e = 0; e < 4; ++e) {
+        y[c][e] = mul2(y[c][e], q2);
+        u[e] = mul2(d[c][e], mul2(y[c][e], f[e]));   // d u
+        z1 = add2(z1, u[e]);
+        d[c][e] = mul2(d[c][e], g[e]);               // du
+        if (a.gate_mode == MOE_GATE_CHANNEL) sg[c][e] = add2(sg[c][e], u[e]);
+        if (a.norm_y) sw[c][e] = fma2(d[c][e], y[c][e], sw[c][e]);
+        d[c][e] = mul2(d[c][e], f[e]);
+        z0 = fma2(d[c][e], y[c][e], z0);
       }
       if (a.gate_mode == MOE_GATE_FULL && a.dgate)
-        store8<VEC>(static_cast<T*>(a.dgate) + t * a.lddg, c, nt, tid, H, g);
+        store8<VEC>(static_cast<T*>(a.dgate) + t * a.lddg, c, nt, tid, H, u);
     }
+    float z[2] = {sum_of(z0), sum_of(z1)};
     if (a.norm_y || a.gate_mode == MOE_GATE_TOKEN) {
       block_sums<2>(z, buf[flip]);
       flip ^= 1;
     }
     if (a.gate_mode == MOE_GATE_TOKEN && a.dgate && tid == 0) static_cast<float*>(a.dgate)[t] = z[1];
-    const float m = a.norm_y ? z[0] * inv_h : 0.f;
+    const float m = a.norm_y ? -(z[0] * inv_h) : 0.f;
+    const F2 m2 = f2(m, m);
 #pragma unroll
     for (int c = 0; c < NC; ++c) {
+      if (a.norm_y) {
 #pragma unroll
-      for (int e = 0; e < 8; ++e) d[c][e] = a.norm_y ? q * (d[c][e] - y[c][e] * m) : d[c][e];
+        for (int e = 0; e < 4; ++e) d[c][e] = mul2(q2, fma2(y[c][e], m2, d[c][e]));
+      }
       store8<VEC>(static_cast<T*>(a.dy) + t * a.lddy, c, nt, tid, H, d[c]);
     }
   }
@@ -260,11 +273,12 @@ __global__ void __launch_bounds__(MAXT, MAXT <= 256 ? 2 : 1) norm_backward_kerne
     float* o = gridDim.x == 1 ? out[i] : a.part + ((int64_t)blockIdx.x * kSums + i) * a.part_ld;
 #pragma unroll
     for (int c = 0; c < NC; ++c) {
-      const float(&v)[8] = i == 0 ? sw[c] : i == 1 ? sg[c] : sn[c];
+      Raw8<float> v;
+      from_pairs(i == 0 ? sw[c] : i == 1 ? sg[c] : sn[c], v);
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
         const int n = col_of<VEC>(c, e, nt, tid);
-        if (n < H) o[n] = v[e];
+        if (n < H) o[n] = v.v[e];
       }
     }
   }
@@ -310,14 +324,24 @@ __global__ void __launch_bounds__(1024) norm_sums_kernel(const float* __restrict
 
 // ---- host side ----
 
-// Threads and chunks per thread for rows of H values.
+// Threads and chunks per thread for rows of H values, and rows of a block.
 struct Shape {
-  int nt, nc;
+  int nt, nc, ny;
 };
-Shape shape_of(int H, int most) {
-  const int nt = row_threads(H, most);
-  if (H <= 8 * nt) return {nt, 1};
-  return {row_threads(ceil_div(H, 2), 1024), 2};
+// Backward: one row at a time, one chunk up to 8192 values.
+Shape shape_of(int H) {
+  const int nt = row_threads(H, 1024);
+  if (H <= 8 * nt) return {nt, 1, 1};
+  return {row_threads(ceil_div(H, 2), 1024), 2, 1};
+}
+// Forward, up to 4096 values: 256 threads, with two chunks per thread (half as many exchanges per row,
+// twice the loads in flight per thread: T = 2048, H = 2048, bf16, post with next norm 6.2 us against
+// 7.1), but one up to 256 rows of 2048 values, where a row's own latency counts (2.2 against 2.4 at
+// T = 1). Wider rows take more threads.
+Shape shape_forward(int rows, int H) {
+  if (H > 4096) return shape_of(H);
+  const int nc = H <= 256 || (H <= 2048 && rows <= 256) ? 1 : 2, nt = row_threads(ceil_div(H, nc), 256);
+  return {nt, nc, 256 / nt < kBlockRows ? 256 / nt : kBlockRows};
 }
 
 // Calls f(typed null pointer) for the row type.
@@ -380,16 +404,26 @@ bool gate16(const void* gate, int mode, int64_t ld, size_t z) {
 
 template <typename T, typename YT, bool FUSED>
 int launch_post(const PostArgs& a, int rows, bool vec, cudaStream_t s) {
-  const Shape sh = shape_of(a.H, 1024);
-  // a block of up to 256 threads has the registers for eight choices' words at a time, a larger one
-  // for four
-  constexpr int F8 = FUSED ? 8 : 0, F4 = FUSED ? 4 : 0;
-  auto kern = sh.nc == 2 ? (vec ? norm_post_kernel<T, YT, F4, true, 2, 1024> : norm_post_kernel<T, YT, F4, false, 2, 1024>)
-              : !FUSED || sh.nt > 256
-                  ? (vec ? norm_post_kernel<T, YT, F4, true, 1, 1024> : norm_post_kernel<T, YT, F4, false, 1, 1024>)
-                  : (vec ? norm_post_kernel<T, YT, F8, true, 1, 256> : norm_post_kernel<T, YT, F4, false, 1, 256>);
+  const Shape sh = shape_forward(rows, a.H);
+  // choices read at a time: eight with one chunk per thread, for few tokens; with two chunks four, or
+  // two where there are no more
+  auto pick = [&](auto vec_) {
+    constexpr bool V = decltype(vec_)::value;
+    if constexpr (!FUSED) {
+      if (sh.nt * sh.ny <= 256)
+        return sh.nc == 1 ? norm_post_kernel<T, YT, 0, V, 1, 256> : norm_post_kernel<T, YT, 0, V, 2, 256>;
+      return sh.nc == 1 ? norm_post_kernel<T, YT, 0, V, 1, 1024> : norm_post_kernel<T, YT, 0, V, 2, 1024>;
+    } else {
+      if (sh.nt * sh.ny <= 256) {
+        if (sh.nc == 1) return norm_post_kernel<T, YT, V ? 8 : 4, V, 1, 256>;
+        return a.k <= 2 ? norm_post_kernel<T, YT, 2, V, 2, 256> : norm_post_kernel<T, YT, 4, V, 2, 256>;
+      }
+      return sh.nc == 1 ? norm_post_kernel<T, YT, 4, V, 1, 1024> : norm_post_kernel<T, YT, 2, V, 2, 1024>;
+    }
+  };
+  auto kern = vec ? pick(std::true_type()) : pick(std::false_type());
   note_launch();
-  return check_cuda(launch_pdl(kern, dim3(rows), dim3(sh.nt), 0, s, a), "norm_post_kernel");
+  return check_cuda(launch_pdl(kern, dim3(ceil_div(rows, sh.ny)), dim3(sh.nt, sh.ny), 0, s, a), "norm_post_kernel");
 }
 
 // Checks common to moe_norm_post and moe_combine_norm_post; *vec receives whether rows move as words.
@@ -434,7 +468,7 @@ int launch_back(const char* me, BackArgs& a, int dtype, bool vec, void* ws, size
         if (int rc = check_cuda(cudaMemsetAsync(p, 0, sizeof(float) * a.H, s), me)) return rc;
     return MOE_OK;
   }
-  const Shape sh = shape_of(a.H, 1024);
+  const Shape sh = shape_of(a.H);
   // the ring wants three stages (two rows ahead) and takes up to four; fewer blocks share an SM where
   // that needs their shared memory. Two always fit: five fp32 tensors of 512 * 8 values are 80 KB.
   const int tensors = (a.dho ? 1 : 0) + (a.has_y ? 1 : 0) + (a.next ? 2 : 0) + (a.gate_mode == MOE_GATE_FULL ? 1 : 0);
@@ -492,15 +526,19 @@ MOE_API int moe_norm_pre(const void* h, int64_t h_stride, int dtype, const void*
   if (T == 0) return MOE_OK;
   const size_t z = dtype_size(dtype);
   const bool vec = H % 8 == 0 && rows16(h, h_stride, z) && rows16(x, x_stride, z) && rows16(w, 0, z);
-  const Shape sh = shape_of(H, 1024);
+  const Shape sh = shape_forward(T, H);
   note_launch();
   return by_type(dtype, [&](auto* p) {
     using T_ = std::remove_pointer_t<decltype(p)>;
-    auto kern = sh.nc == 1 ? (vec ? norm_pre_kernel<T_, true, 1> : norm_pre_kernel<T_, false, 1>)
-                           : (vec ? norm_pre_kernel<T_, true, 2> : norm_pre_kernel<T_, false, 2>);
-    return check_cuda(launch_pdl(kern, dim3(T), dim3(sh.nt), 0, reinterpret_cast<cudaStream_t>(stream),
-                                 static_cast<const T_*>(h), h_stride, static_cast<const T_*>(w), eps, H,
-                                 static_cast<T_*>(x), x_stride),
+    auto pick = [&](auto vec_) {
+      constexpr bool V = decltype(vec_)::value;
+      if (sh.nt * sh.ny <= 256) return sh.nc == 1 ? norm_pre_kernel<T_, V, 1, 256> : norm_pre_kernel<T_, V, 2, 256>;
+      return sh.nc == 1 ? norm_pre_kernel<T_, V, 1, 1024> : norm_pre_kernel<T_, V, 2, 1024>;
+    };
+    auto kern = vec ? pick(std::true_type()) : pick(std::false_type());
+    return check_cuda(launch_pdl(kern, dim3(ceil_div(T, sh.ny)), dim3(sh.nt, sh.ny), 0,
+                                 reinterpret_cast<cudaStream_t>(stream), static_cast<const T_*>(h), h_stride,
+                                 static_cast<const T_*>(w), eps, T, H, static_cast<T_*>(x), x_stride),
                       "norm_pre_kernel");
   });
 }
@@ -535,7 +573,7 @@ MOE_API int moe_norm_post(const void* y, int64_t y_stride, const void* h, int64_
   const char* me = "moe_norm_post";
   PostArgs a{};
   a.y = y; a.ldy = y_stride; a.h = h; a.ldh = h_stride; a.w = w; a.gate = gate; a.ldg = gate_stride;
-  a.gate_mode = gate_mode; a.alpha = alpha; a.eps = eps; a.H = H;
+  a.gate_mode = gate_mode; a.alpha = alpha; a.eps = eps; a.T = T; a.H = H;
   a.norm_y = (flags & MOE_NORM_Y) != 0; a.next = (flags & MOE_NORM_NEXT) != 0;
   a.h_out = h_out; a.ldho = h_out_stride; a.w_next = w_next; a.x_next = x_next; a.ldx = x_next_stride;
   bool vec = false;
@@ -558,7 +596,7 @@ MOE_API int moe_combine_norm_post(const void* yp, int64_t yp_stride, int yp_dtyp
   const char* me = "moe_combine_norm_post";
   PostArgs a{};
   a.y = yp; a.ldy = yp_stride; a.h = h; a.ldh = h_stride; a.w = w; a.gate = gate; a.ldg = gate_stride;
-  a.gate_mode = gate_mode; a.alpha = alpha; a.eps = eps; a.H = H;
+  a.gate_mode = gate_mode; a.alpha = alpha; a.eps = eps; a.T = T; a.H = H;
   a.norm_y = (flags & MOE_NORM_Y) != 0; a.next = (flags & MOE_NORM_NEXT) != 0;
   a.h_out = h_out; a.ldho = h_out_stride; a.w_next = w_next; a.x_next = x_next; a.ldx = x_next_stride;
   a.y_out = y_out; a.ldyo = y_out_stride; a.inv = inv; a.wts = wts; a.k = k;

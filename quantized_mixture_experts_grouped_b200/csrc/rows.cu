@@ -262,17 +262,19 @@ int dispatch_units(const void* x, int64_t ldx, const int32_t* idx, int T, int E,
 
 // ------------------------------------------------------------------------------------- combine
 
-template <typename YT, typename OT, bool VEC, int B>
-__global__ void __launch_bounds__(kRowThreads) combine_rows_kernel(const YT* __restrict__ yp, int64_t ldy,
+template <typename YT, typename OT, bool VEC, int B, int NC>
+__global__ void __launch_bounds__(kRowThreads, VEC && sizeof(YT) == 2 ? 4 : 1) combine_rows_kernel(const YT* __restrict__ yp, int64_t ldy,
                                                                    const int32_t* __restrict__ inv,
-                                                                   const float* __restrict__ wts, int k, int P, int H,
-                                                                   OT* __restrict__ out, int64_t ldo) {
+                                                                   const float* __restrict__ wts, int T, int k, int P,
+                                                                   int H, OT* __restrict__ out, int64_t ldo) {
   pdl_begin();
-  const int64_t t = blockIdx.x;
-  float v[8];
-  weighted_rows<B, VEC>(yp, ldy, inv + t * k, wts ? wts + t * k : nullptr, k, P, blockIdx.y, blockDim.x, threadIdx.x, H,
-                     v);
-  store8<VEC>(out + t * ldo, blockIdx.y, blockDim.x, threadIdx.x, H, v);
+  const int64_t t = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
+  if (t >= T) return;
+  F2 v[NC][4];
+  weighted_rows<B, NC, VEC>(yp, ldy, inv + t * k, wts ? wts + t * k : nullptr, k, P, blockIdx.y * NC, blockDim.x,
+                            threadIdx.x, H, v);
+#pragma unroll
+  for (int c = 0; c < NC; ++c) store8<VEC>(out + t * ldo, blockIdx.y * NC + c, blockDim.x, threadIdx.x, H, v[c]);
 }
 
 // Gradient of combine: one block per token. dout's row stays in registers while the token's rows
@@ -296,20 +298,22 @@ __global__ void __launch_bounds__(kRowThreads, VEC ? 4 : 2) combine_backward_ker
   const float* wt = wts + t * k;
   int flip = 0;
   for (int j0 = 0; j0 < k; j0 += kDots, flip ^= 1) {
-    float dot[kDots], w[kDots];
+    float w[kDots];
     int pos[kDots];
 #pragma unroll
     for (int b = 0; b < kDots; ++b) {
       const bool in = j0 + b < k;
       pos[b] = in ? it[j0 + b] : -1;
       w[b] = in ? wt[j0 + b] : 0.f;
-      dot[b] = 0.f;
     }
 #pragma unroll
     for (int b = 0; b < kDots; ++b)
       if ((unsigned)pos[b] >= (unsigned)P) pos[b] = -1;
+    F2 part[kDots];
+#pragma unroll
+    for (int b = 0; b < kDots; ++b) part[b] = f2(0.f, 0.f);
     for (int c = 0; c < chunks; ++c) {
-      float d[8];
+      F2 d[4];
       load8<VEC>(dout + t * ldo, c, nt, tid, H, d);
       // four choices' words at a time and four blocks per SM: T = 2048, k = 8, H = 2048 took 54 us for
       // the whole gradient with eight and three, 49 with four and five (spills), 44 like this
@@ -328,22 +332,31 @@ __global__ void __launch_bounds__(kRowThreads, VEC ? 4 : 2) combine_backward_ker
         if (dyp) {          // does not wait for yp's rows
 #pragma unroll
           for (int b = 0; b < B; ++b) {
-            float g[8];
+            if (j0 + b0 + b >= k) break;
+            const F2 w2 = f2(w[b0 + b], w[b0 + b]);
+            F2 g[4];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) g[e] = w[b0 + b] * d[e];
+            for (int e = 0; e < 4; ++e) g[e] = mul2(w2, d[e]);
             const bool on = pos[b0 + b] >= 0;
             store8<VEC>(dyp + (int64_t)(on ? pos[b0 + b] : 0) * lddy, c, nt, tid, on ? H : 0, g);
           }
         }
         if (dwts) {
 #pragma unroll
-          for (int b = 0; b < B; ++b)
+          for (int b = 0; b < B; ++b) {
+            if (j0 + b0 + b >= k) break;
+            F2 v[4];
+            to_pairs(r[b], v);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) dot[b0 + b] = fmaf(d[e], RowType<YT>::to(r[b].v[e]), dot[b0 + b]);
+            for (int e = 0; e < 4; ++e) part[b0 + b] = fma2(d[e], v[e], part[b0 + b]);
+          }
         }
       }
     }
     if (dwts) {
+      float dot[kDots];
+#pragma unroll
+      for (int b = 0; b < kDots; ++b) dot[b] = sum_of(part[b]);
       block_sums<kDots>(dot, buf[flip]);
 #pragma unroll
       for (int b = 0; b < kDots; ++b)
@@ -429,17 +442,23 @@ int launch_combine_rows(const void* yp, int64_t ldy, int ydt, const int32_t* inv
                         void* out, int64_t ldo, int odt, cudaStream_t s) {
   if (T == 0) return MOE_OK;
   const bool vec = H % 8 == 0 && rows16(yp, ldy, dtype_size(ydt)) && rows16(out, ldo, dtype_size(odt));
-  const int nt = row_threads(H, kRowThreads);
-  const dim3 grid(T, ceil_div(H, 8 * nt));
+  // More than four choices: eight at a time, one chunk per thread (2048 tokens of 8 choices, H = 2048:
+  // 34.4 us sort and copy included, 35.5 as two chunks of four). Fewer: two chunks of two or four (8192
+  // tokens of 2, H = 2048: 27 us with four places for two choices, 23 with two). Single values: one
+  // chunk of four. Narrow rows share a block.
+  const bool eight = vec && k > 4, two = vec && !eight && H > 256;
+  const int nt = row_threads(ceil_div(H, two ? 2 : 1), kRowThreads), ny = kRowThreads / nt;
+  const dim3 grid(ceil_div(T, ny), ceil_div(H, 8 * nt * (two ? 2 : 1)));
   note_launch();
   return by_types(ydt, odt, [&](auto* y, auto* o) {
     using YT = std::remove_pointer_t<decltype(y)>;
     using OT = std::remove_pointer_t<decltype(o)>;
-    // single values fill the registers with four choices; few choices need no more either
-    auto kern = !vec ? combine_rows_kernel<YT, OT, false, 4>
-                     : k > 4 ? combine_rows_kernel<YT, OT, true, 8> : combine_rows_kernel<YT, OT, true, 4>;
-    return check_cuda(launch_pdl(kern, grid, dim3(nt), 0, s, static_cast<const YT*>(yp), ldy, inv, wts, k, T * k, H,
-                                 static_cast<OT*>(out), ldo),
+    auto kern = !vec ? combine_rows_kernel<YT, OT, false, 4, 1>
+                : eight ? combine_rows_kernel<YT, OT, true, 8, 1>
+                : !two ? combine_rows_kernel<YT, OT, true, 4, 1>
+                : k <= 2 ? combine_rows_kernel<YT, OT, true, 2, 2> : combine_rows_kernel<YT, OT, true, 4, 2>;
+    return check_cuda(launch_pdl(kern, grid, dim3(nt, ny), 0, s, static_cast<const YT*>(yp), ldy, inv, wts, T, k, T * k,
+                                 H, static_cast<OT*>(out), ldo),
                       "combine_rows_kernel");
   });
 }

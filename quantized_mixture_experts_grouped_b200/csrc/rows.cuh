@@ -54,41 +54,6 @@ __device__ __forceinline__ Raw8<T> load_raw(const T* row, int c, int nt, int tid
   return r;
 }
 
-template <typename T>
-__device__ __forceinline__ void to_float(const Raw8<T>& r, float (&f)[8]) {
-#pragma unroll
-  for (int e = 0; e < 8; ++e) f[e] = RowType<T>::to(r.v[e]);
-}
-
-template <bool VEC, typename T>
-__device__ __forceinline__ void load8(const T* row, int c, int nt, int tid, int H, float (&f)[8]) {
-  to_float(load_raw<VEC>(row, c, nt, tid, H), f);
-}
-
-template <typename T>
-__device__ __forceinline__ void store_raw(T* row, int n0, int H, const Raw8<T>& r) {
-  if (n0 >= H) return;
-  const uint4* q = reinterpret_cast<const uint4*>(&r);
-#pragma unroll
-  for (int i = 0; i < (int)sizeof(T) / 2; ++i) reinterpret_cast<uint4*>(row + n0)[i] = q[i];
-}
-
-template <bool VEC, typename T>
-__device__ __forceinline__ void store8(T* row, int c, int nt, int tid, int H, const float (&f)[8]) {
-  Raw8<T> r;
-#pragma unroll
-  for (int e = 0; e < 8; ++e) r.v[e] = RowType<T>::from(f[e]);
-  if (VEC) {
-    store_raw(row, col_of<true>(c, 0, nt, tid), H, r);
-  } else {
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const int n = col_of<false>(c, e, nt, tid);
-      if (n < H) row[n] = r.v[e];
-    }
-  }
-}
-
 // Two fp32 values in one 64-bit register pair: the sm_100 packed forms do both in one instruction.
 // The row kernels with long arithmetic per value are bound by issued instructions, which these halve;
 // each half rounds as the scalar operation does.
@@ -157,6 +122,34 @@ __device__ __forceinline__ void from_pairs(const F2 (&f)[4], Raw8<float>& r) {
   }
 }
 
+template <bool VEC, typename T>
+__device__ __forceinline__ void load8(const T* row, int c, int nt, int tid, int H, F2 (&f)[4]) {
+  to_pairs(load_raw<VEC>(row, c, nt, tid, H), f);
+}
+
+template <typename T>
+__device__ __forceinline__ void store_raw(T* row, int n0, int H, const Raw8<T>& r) {
+  if (n0 >= H) return;
+  const uint4* q = reinterpret_cast<const uint4*>(&r);
+#pragma unroll
+  for (int i = 0; i < (int)sizeof(T) / 2; ++i) reinterpret_cast<uint4*>(row + n0)[i] = q[i];
+}
+
+template <bool VEC, typename T>
+__device__ __forceinline__ void store8(T* row, int c, int nt, int tid, int H, const F2 (&f)[4]) {
+  Raw8<T> r;
+  from_pairs(f, r);
+  if (VEC) {
+    store_raw(row, col_of<true>(c, 0, nt, tid), H, r);
+  } else {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const int n = col_of<false>(c, e, nt, tid);
+      if (n < H) row[n] = r.v[e];
+    }
+  }
+}
+
 // N sums over the block (N = 1, 2, 3, 4 or 8), every thread gets them, in an order fixed by the
 // block size. The lanes of a warp share the values out between them as they add (half of the values
 // to each half-warp, and so on), so 4 sums cost 6 exchanges and not 20. One barrier per call: `buf`
@@ -205,18 +198,20 @@ __device__ __forceinline__ void block_sums(float (&v)[N], float* buf) {
   }
 }
 
-// out = sum over j of w[j] * rows[inv[j]] (chunk c of a token), in j order; a choice whose inv is
-// outside [0, P) adds nothing. The places and weights of a batch of choices are read before the
+// out[c] = sum over j of w[j] * rows[inv[j]] (chunks c0 to c0 + NC - 1 of a token), in j order; a choice
+// whose inv is outside [0, P) adds nothing. The places and weights of B choices are read before the
 // first of their rows, and the rows before the first is used, so that one token waits for memory
 // twice and not twice per choice (2048 tokens, 8 choices, H = 2048: 44 us when each row waited for
-// its own place). B: choices read at a time.
-template <int B, bool VEC, typename T>
+// its own place).
+template <int B, int NC, bool VEC, typename T>
 __device__ __forceinline__ void weighted_rows(const T* rows, int64_t ld, const int32_t* inv, const float* wts, int k,
-                                              int P, int c, int nt, int tid, int H, float (&out)[8]) {
+                                              int P, int c0, int nt, int tid, int H, F2 (&out)[NC][4]) {
 #pragma unroll
-  for (int e = 0; e < 8; ++e) out[e] = 0.f;
+  for (int c = 0; c < NC; ++c)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) out[c][e] = f2(0.f, 0.f);
   for (int j0 = 0; j0 < k; j0 += B) {
-    Raw8<T> r[B];
+    Raw8<T> r[B][NC];
     float w[B];
     int p[B];
 #pragma unroll
@@ -230,12 +225,22 @@ __device__ __forceinline__ void weighted_rows(const T* rows, int64_t ld, const i
       const bool on = (unsigned)p[b] < (unsigned)P;
       // a choice left out reads nothing (H = 0) and counts with weight 0 on zeros
       w[b] = on ? w[b] : 0.f;
-      r[b] = load_raw<VEC>(rows + (int64_t)(on ? p[b] : 0) * ld, c, nt, tid, on ? H : 0);
+      const T* row = rows + (int64_t)(on ? p[b] : 0) * ld;
+#pragma unroll
+      for (int c = 0; c < NC; ++c) r[b][c] = load_raw<VEC>(row, c0 + c, nt, tid, on ? H : 0);
     }
 #pragma unroll
-    for (int b = 0; b < B; ++b)
+    for (int b = 0; b < B; ++b) {
+      if (j0 + b >= k) break;
+      const F2 w2 = f2(w[b], w[b]);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) out[e] = fmaf(w[b], RowType<T>::to(r[b].v[e]), out[e]);
+      for (int c = 0; c < NC; ++c) {
+        F2 v[4];
+        to_pairs(r[b][c], v);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) out[c][e] = fma2(w2, v[e], out[c][e]);
+      }
+    }
   }
 }
 
