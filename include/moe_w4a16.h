@@ -234,8 +234,8 @@ int moe_bf16_layer(const uint16_t* x_bf16, const uint16_t* logits_bf16,
 /* ---- Rows sorted by expert and back (for expert products of the caller's own: unquantised,
  * adapted or trained experts between the same router and the same combine), with their gradients.
  *
- * Rows are bf16, fp16 or fp32 (MOE_DTYPE_*), H values each, any H >= 1; *_stride is the distance
- * between rows in elements (inputs: >= 0, 0 repeats one row; outputs: >= H). Rows that start on
+ * Rows are bf16, fp16 or fp32 (MOE_DTYPE_*), H values each, H from 1 to 2^30; *_stride is the
+ * distance between rows in elements (inputs: >= 0, 0 repeats one row; outputs: >= H). Rows that start on
  * 16-byte boundaries with H a multiple of 8 move as 16-byte words, others value by value. Sums are
  * fp32 in a fixed order (results are bit-identical run to run), rounded once. Outputs must not
  * overlap inputs unless a comment allows it. T = 0 is a valid empty batch. */
@@ -246,7 +246,8 @@ enum { MOE_DTYPE_BF16 = 0, MOE_DTYPE_F16 = 1, MOE_DTYPE_F32 = 2 };
  * An id outside [0, E) drops its pair (a choice over an expert's capacity): inv = -1, no row. The
  * kept rows are the first offsets[E]; perm and xp behind them are left as they were. A batch of
  * at most 2048 pairs is one launch, a larger one two.
- * Errors: MOE_ERR_ARG, MOE_ERR_SHAPE (E > 256, T*k > 2^31-1). */
+ * Errors of this and the next calls: MOE_ERR_ARG, MOE_ERR_SHAPE (E > 256, H > 2^30, T*k > 2^31-1),
+ * MOE_ERR_CUDA. */
 int moe_dispatch(const void* x, int64_t x_stride, int dtype, const int32_t* idx,
                  int T, int H, int E, int k,
                  int32_t* counts, int32_t* offsets, int32_t* perm, int32_t* inv,

@@ -99,7 +99,8 @@ __global__ void __launch_bounds__(MAXT) norm_pre_kernel(const T* __restrict__ h,
 // a thread reads its values of the row before it writes them, and no other thread reads them.
 // FUSED: the choices read at a time, 0 for rows that are y itself.
 template <typename T, typename YT, int FUSED, bool VEC, int NC, int MAXT>
-__global__ void __launch_bounds__(MAXT, MAXT == 256 && VEC && !FUSED && NC == 1 ? 8 : 1) norm_post_kernel(const PostArgs a) {
+__global__ void __launch_bounds__(MAXT, MAXT == 256 && VEC && !FUSED ? (NC == 1 ? 8 : 4) : 1)
+    norm_post_kernel(const PostArgs a) {
   __shared__ float buf[2][kBlockRows][32];
   pdl_begin();
   const int64_t t = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
@@ -287,17 +288,20 @@ __global__ void __launch_bounds__(MAXT, MAXT <= 256 ? 2 : 1) norm_backward_kerne
 // Adds the blocks' partial sums: a block has 32 columns (8 lanes of 16 bytes) by 128 runs, run i
 // taking the blocks i, i + 128, ... in order; then the runs are added in a fixed tree. With 19 blocks
 // after one another per run and single values the sums of 592 blocks took 4.5 us.
+struct Sums {
+  float* out[kSums];               // the sums asked for, and which of the partial sums each is
+  int which[kSums];
+};
 __global__ void __launch_bounds__(1024) norm_sums_kernel(const float* __restrict__ part, int blocks, int H, int ld,
-                                                         float* o0, float* o1, float* o2) {
+                                                         const Sums s) {
   __shared__ float sum[32][33];
   pdl_begin();
-  float* out = blockIdx.y == 0 ? o0 : blockIdx.y == 1 ? o1 : o2;
-  if (!out) return;
+  float* out = s.out[blockIdx.y];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, run = threadIdx.x >> 3;
   const int n = blockIdx.x * 32 + (lane & 7) * 4;
   float v[4] = {0.f, 0.f, 0.f, 0.f};
   if (n < H) {
-    const float* p = part + (int64_t)blockIdx.y * ld + n;
+    const float* p = part + (int64_t)s.which[blockIdx.y] * ld + n;
 #pragma unroll 5
     for (int b = run; b < blocks; b += 128) {
       const float4 x = *reinterpret_cast<const float4*>(p + (int64_t)b * kSums * ld);
@@ -496,9 +500,16 @@ int launch_back(const char* me, BackArgs& a, int dtype, bool vec, void* ws, size
     return check_cuda(launch_pdl(kern, dim3(blocks), dim3(sh.nt), 0, s, a), "norm_backward_kernel");
   });
   if (rc || !any || blocks == 1) return rc;
+  Sums asked{};
+  int n = 0;
+  for (int i = 0; i < kSums; ++i) {
+    if (!sums[i]) continue;
+    asked.out[n] = sums[i];
+    asked.which[n++] = i;
+  }
   note_launch();
-  return check_cuda(launch_pdl(norm_sums_kernel, dim3(ceil_div(a.H, 32), kSums), dim3(1024), 0, s,
-                               (const float*)a.part, blocks, a.H, a.part_ld, sums[0], sums[1], sums[2]),
+  return check_cuda(launch_pdl(norm_sums_kernel, dim3(ceil_div(a.H, 32), n), dim3(1024), 0, s, (const float*)a.part,
+                               blocks, a.H, a.part_ld, asked),
                     "norm_sums_kernel");
 }
 

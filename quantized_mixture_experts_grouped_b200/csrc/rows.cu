@@ -466,6 +466,7 @@ int launch_combine_rows(const void* yp, int64_t ldy, int ydt, const int32_t* inv
 int check_rows(const char* what, int T, int H, int k) {
   if (T < 0 || H < 1 || k < 1) return fail(MOE_ERR_ARG, "%s: bad sizes T=%d H=%d k=%d", what, T, H, k);
   if ((int64_t)T * k > INT32_MAX) return fail(MOE_ERR_SHAPE, "%s: T*k exceeds 2^31-1", what);
+  if (H > 1 << 30) return fail(MOE_ERR_SHAPE, "%s: H=%d exceeds 2^30", what, H);   // column numbers are ints
   return MOE_OK;
 }
 

@@ -340,3 +340,69 @@ def test_binding_refusals_on_device():
         with pytest.raises(q.MoeError) as ei:
             call()
         assert ei.value.code == q.MOE_ERR_ARG, n
+
+
+def test_first_call_of_a_process_is_captured():
+    """A process whose first calls are captured into a graph: nothing of them needs a warm-up."""
+    import os
+    import subprocess
+    import sys
+    code = """
+import torch, quantized_mixture_experts_grouped_b200 as q
+T, k, E, H = 400, 8, 16, 512
+x = torch.randn(T, H, device="cuda").bfloat16()
+idx = torch.rand(T, E, device="cuda").argsort(1)[:, :k].int().contiguous()
+w = torch.ones(T, k, device="cuda")
+i = dict(dtype=torch.int32, device="cuda")
+c, o, p, inv = torch.empty(E, **i), torch.empty(E + 1, **i), torch.empty(T * k, **i), torch.empty(T, k, **i)
+xp, out, dh, dw = torch.empty(T * k, H, device="cuda").bfloat16(), x.clone(), x.clone(), torch.empty(H, device="cuda")
+ws = torch.empty(q.moe_norm_workspace_bytes(T, H), dtype=torch.uint8, device="cuda")
+torch.cuda.synchronize()
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    q.moe_dispatch(x, idx, E, c, o, p, inv, xp)
+    q.moe_combine(xp, inv, w, out)
+    q.moe_norm_pre_backward(out, x, None, 1e-5, dh, dw=dw, ws=ws)
+g.replay()
+torch.cuda.synchronize()
+assert torch.equal(out, x * 8) and torch.isfinite(dh).all() and torch.isfinite(dw).all()
+"""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0, r.stderr[-2000:]
+
+
+def test_two_threads_at_once():
+    """Two host threads with streams of their own, both sorting, combining and norming in a loop."""
+    import threading
+    jobs = []
+    for s in range(2):
+        g = torch.Generator().manual_seed(20 + s)
+        T, E, k, H = 300 + 77 * s, 16, 4, 512
+        idx, wts = routing(T, E, k, g, 0.1)
+        jobs.append((rows(T, H, torch.bfloat16, g), idx, E, wts.cuda(), torch.cuda.Stream()))
+    want = []
+    for x, idx, E, w, _ in jobs:
+        o = dispatch(x, idx, E)
+        out = room(*x.shape, x.dtype)
+        q.moe_combine(o["xp"], o["inv"], w, out)
+        want.append((o["inv"].clone(), out))
+    torch.cuda.synchronize()
+    wrong = []
+
+    def work(n):
+        x, idx, E, w, s = jobs[n]
+        with torch.cuda.stream(s):
+            for _ in range(50):
+                o = dispatch(x, idx, E)
+                out = room(*x.shape, x.dtype)
+                q.moe_combine(o["xp"], o["inv"], w, out)
+                s.synchronize()
+                if not (torch.equal(o["inv"], want[n][0]) and torch.equal(out, want[n][1])):
+                    wrong.append(n)
+    threads = [threading.Thread(target=work, args=(n,)) for n in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not wrong
