@@ -483,7 +483,8 @@ int launch_back(const char* me, BackArgs& a, int dtype, bool vec, void* ws, size
   const int fit = kRingBytes / per_sm / stage_bytes;
   const int stages = fit < kRingStages ? fit : kRingStages;
   const bool use_ring = vec && sh.nc == 1 && sh.nt <= kRingThreads && stages >= 2;
-  const int blocks = back_blocks(a.T, a.H, per_sm);
+  // sums over one or two rows take no second launch: one block (two rows of 2048: 2.9 us against 3.7)
+  const int blocks = any && a.T <= 2 ? 1 : back_blocks(a.T, a.H, per_sm);
   a.part_ld = part_stride(a.H);
   if (any && blocks > 1) {
     const size_t need = norm_ws(a.T, a.H);
