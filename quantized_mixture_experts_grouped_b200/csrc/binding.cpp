@@ -85,7 +85,8 @@ class Call {
     r.dtype = dtype_code(t.scalar_type());
     if (r.dtype < 0 || (dtype >= 0 && r.dtype != dtype))
       refuse(std::string(what) + " is " + c10::toString(t.scalar_type()));
-    if (r.n > 0 && r.width > 1 && t.stride(1) != 1) refuse("the values of a row of " + std::string(what) + " are not neighbours");
+    if (r.n > 0 && r.width > 1 && t.stride(1) != 1)
+      refuse("the values of a row of " + std::string(what) + " are not neighbours");
     r.ld = r.n > 1 ? t.stride(0) : r.width;
     r.p = t.data_ptr();
     return r;
@@ -106,7 +107,8 @@ class Call {
       for (int64_t s : sizes) want += "[" + (s < 0 ? std::string("any") : std::to_string(s)) + "]";
       refuse(std::string(what) + " is not of shape " + want);
     }
-    if (t.scalar_type() != type) refuse(std::string(what) + " is " + c10::toString(t.scalar_type()) + ", expected " + c10::toString(type));
+    if (t.scalar_type() != type)
+      refuse(std::string(what) + " is " + c10::toString(t.scalar_type()) + ", expected " + c10::toString(type));
     if (!t.is_contiguous()) refuse(std::string(what) + " is not contiguous");
     return t.data_ptr();
   }
@@ -391,7 +393,8 @@ PyObject* norm_post_backward(PyObject* const* args, Py_ssize_t n) {
   Call c("moe_norm_post_backward", args, n, 17);
   const Rows d = c.rows(0, "dh_out");
   const int64_t T = d.n, H = d.width;
-  const Rows y = c.rows(1, "y", T, H, d.dtype), dh = c.rows(2, "dh", T, H, d.dtype), dy = c.rows(3, "dy", T, H, d.dtype);
+  const Rows y = c.rows(1, "y", T, H, d.dtype), dh = c.rows(2, "dh", T, H, d.dtype),
+             dy = c.rows(3, "dy", T, H, d.dtype);
   const float eps = (float)c.number(4), alpha = (float)c.number(5);
   const bool norm_y = c.truth(6), next = !c.none(13);
   if (!next && (!c.none(11) || !c.none(12) || !c.none(14))) c.refuse("h_out, w_next or dw_next without dx_next");
@@ -411,8 +414,8 @@ PyObject* norm_post_backward(PyObject* const* args, Py_ssize_t n) {
   void* ws = c.workspace(15, &bytes);
   const int flags = (norm_y ? MOE_NORM_Y : 0) | (next ? MOE_NORM_NEXT : 0);
   return c.run(16, [&](moe_stream_t s) {
-    return moe_norm_post_backward(d.p, d.ld, y.p, y.ld, d.dtype, w, g.p, g.ld, g.mode, alpha, eps, (int)T, (int)H, flags,
-                                  ho.p, ho.ld, wn, dx.p, dx.ld, dh.p, dh.ld, dy.p, dy.ld, dw, const_cast<void*>(dg.p),
+    return moe_norm_post_backward(d.p, d.ld, y.p, y.ld, d.dtype, w, g.p, g.ld, g.mode, alpha, eps, (int)T, (int)H,
+                                  flags, ho.p, ho.ld, wn, dx.p, dx.ld, dh.p, dh.ld, dy.p, dy.ld, dw, const_cast<void*>(dg.p),
                                   dg.ld, dwn, ws, bytes, s);
   });
 }

@@ -436,7 +436,8 @@ int check_post(const char* me, const PostArgs& a, int T, int H, int dtype, int f
   if (flags & ~(MOE_NORM_Y | MOE_NORM_NEXT)) return fail(MOE_ERR_ARG, "%s: unknown flags %d", me, flags);
   if (int rc = check_gate(me, a.gate, a.gate_mode)) return rc;
   if (T > 0 && (!a.y || !a.h || !a.h_out || (a.next && !a.x_next))) return fail(MOE_ERR_ARG, "%s: null pointer", me);
-  if (T > 0 && ((a.h_out == a.h && a.ldho != a.ldh) || a.h_out == a.y || (a.next && (a.x_next == a.h_out || a.x_next == a.h || a.x_next == a.y))))
+  if (T > 0 && ((a.h_out == a.h && a.ldho != a.ldh) || a.h_out == a.y ||
+                (a.next && (a.x_next == a.h_out || a.x_next == a.h || a.x_next == a.y))))
     return fail(MOE_ERR_ARG, "%s: outputs overlap", me);
   const size_t z = dtype_size(dtype);
   if (int rc = check_ld(me, "h", a.h, a.ldh, T, H, false)) return rc;
@@ -489,7 +490,8 @@ int launch_back(const char* me, BackArgs& a, int dtype, bool vec, void* ws, size
   if (any && blocks > 1) {
     const size_t need = norm_ws(a.T, a.H);
     if (!ws || ws_bytes < need)
-      return fail(MOE_ERR_ARG, "%s: workspace of %zu bytes is smaller than the %zu needed", me, ws ? ws_bytes : 0, need);
+      return fail(MOE_ERR_ARG, "%s: workspace of %zu bytes is smaller than the %zu needed", me, ws ? ws_bytes : 0,
+                  need);
     if (reinterpret_cast<uintptr_t>(ws) & 255) return fail(MOE_ERR_ARG, "%s: workspace must be 256-byte aligned", me);
     a.part = static_cast<float*>(ws);
   }

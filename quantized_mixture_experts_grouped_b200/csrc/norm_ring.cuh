@@ -60,8 +60,8 @@ __device__ __forceinline__ void load_words(const void* base, int nt, int tid, in
 }
 
 template <typename T, int MAXT, bool HAS_Y, bool NORM_Y, bool NEXT, int GATE>
-__global__ void __launch_bounds__(MAXT, ring_blocks(MAXT, HAS_Y)) norm_backward_ring_kernel(const BackArgs a, int stages,
-                                                                                       int stage_bytes) {
+__global__ void __launch_bounds__(MAXT, ring_blocks(MAXT, HAS_Y))
+    norm_backward_ring_kernel(const BackArgs a, int stages, int stage_bytes) {
   extern __shared__ __align__(16) unsigned char ring[];
   __shared__ float buf[2][32 * 4];
   int flip = 0;

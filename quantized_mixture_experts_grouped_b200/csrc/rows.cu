@@ -263,10 +263,9 @@ int dispatch_units(const void* x, int64_t ldx, const int32_t* idx, int T, int E,
 // ------------------------------------------------------------------------------------- combine
 
 template <typename YT, typename OT, bool VEC, int B, int NC>
-__global__ void __launch_bounds__(kRowThreads, VEC && sizeof(YT) == 2 ? 4 : 1) combine_rows_kernel(const YT* __restrict__ yp, int64_t ldy,
-                                                                   const int32_t* __restrict__ inv,
-                                                                   const float* __restrict__ wts, int T, int k, int P,
-                                                                   int H, OT* __restrict__ out, int64_t ldo) {
+__global__ void __launch_bounds__(kRowThreads, VEC && sizeof(YT) == 2 ? 4 : 1)
+    combine_rows_kernel(const YT* __restrict__ yp, int64_t ldy, const int32_t* __restrict__ inv,
+                        const float* __restrict__ wts, int T, int k, int P, int H, OT* __restrict__ out, int64_t ldo) {
   pdl_begin();
   const int64_t t = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
   if (t >= T) return;
@@ -283,12 +282,10 @@ __global__ void __launch_bounds__(kRowThreads, VEC && sizeof(YT) == 2 ? 4 : 1) c
 constexpr int kDots = 8;
 
 template <typename YT, typename OT, bool VEC>
-__global__ void __launch_bounds__(kRowThreads, VEC ? 4 : 2) combine_backward_kernel(const OT* __restrict__ dout, int64_t ldo,
-                                                                       const YT* __restrict__ yp, int64_t ldy,
-                                                                       const int32_t* __restrict__ inv,
-                                                                       const float* __restrict__ wts, int k, int P,
-                                                                       int H, YT* __restrict__ dyp, int64_t lddy,
-                                                                       float* __restrict__ dwts) {
+__global__ void __launch_bounds__(kRowThreads, VEC ? 4 : 2)
+    combine_backward_kernel(const OT* __restrict__ dout, int64_t ldo, const YT* __restrict__ yp, int64_t ldy,
+                            const int32_t* __restrict__ inv, const float* __restrict__ wts, int k, int P, int H,
+                            YT* __restrict__ dyp, int64_t lddy, float* __restrict__ dwts) {
   __shared__ float buf[2][32 * kDots];
   pdl_begin();
   const int64_t t = blockIdx.x;

@@ -144,7 +144,8 @@ def test_post_widths(T, H, dt):
         run_post_backward(T, H, dt, g, 0, y, ho, wi, gt, wni, True, True, 1.0)
 
 
-@pytest.mark.parametrize("T,E,k,H", [(1, 64, 8, 2048), (16, 64, 8, 2048), (5, 7, 3, 1031), (6, 12, 9, 4096), (2, 8, 2, 16384)])
+@pytest.mark.parametrize("T,E,k,H", [(1, 64, 8, 2048), (16, 64, 8, 2048), (5, 7, 3, 1031), (6, 12, 9, 4096),
+                                     (2, 8, 2, 16384), (300, 8, 2, 512), (280, 64, 8, 2048)])
 @pytest.mark.parametrize("ydt,dt", [("bf16", "bf16"), ("f32", "bf16"), ("f16", "f16"), ("f32", "f16"), ("f32", "f32")])
 @pytest.mark.parametrize("norm_y,gate,nxt,drop,pad", [(True, "none", True, 0.0, 0), (True, "channel", True, 0.5, 8),
                                                        (False, "token", False, 0.5, 0), (False, "full", True, 0.0, 1)])
