@@ -99,7 +99,7 @@ __global__ void __launch_bounds__(MAXT) norm_pre_kernel(const T* __restrict__ h,
 // a thread reads its values of the row before it writes them, and no other thread reads them.
 // FUSED: the choices read at a time, 0 for rows that are y itself.
 template <typename T, typename YT, int FUSED, bool VEC, int NC, int MAXT>
-__global__ void __launch_bounds__(MAXT, MAXT == 256 && VEC && !FUSED ? (NC == 1 ? 8 : 4) : 1)
+__global__ void __launch_bounds__(MAXT, MAXT == 256 && VEC ? (NC == 2 ? 4 : FUSED ? 1 : 8) : 1)
     norm_post_kernel(const PostArgs a) {
   __shared__ float buf[2][kBlockRows][32];
   pdl_begin();
@@ -409,8 +409,9 @@ bool gate16(const void* gate, int mode, int64_t ld, size_t z) {
 template <typename T, typename YT, bool FUSED>
 int launch_post(const PostArgs& a, int rows, bool vec, cudaStream_t s) {
   const Shape sh = shape_forward(rows, a.H);
-  // choices read at a time: eight with one chunk per thread, for few tokens; with two chunks four, or
-  // two where there are no more
+  // choices read at a time: eight with one chunk per thread, for few tokens; two with two chunks, which
+  // leaves room for four blocks per SM (T = 2048, k = 8, H = 2048, bf16: 17.2 us, with four at a time in
+  // two blocks 22.3, and moe_combine and moe_norm_post one after the other 20.3)
   auto pick = [&](auto vec_) {
     constexpr bool V = decltype(vec_)::value;
     if constexpr (!FUSED) {
@@ -420,7 +421,7 @@ int launch_post(const PostArgs& a, int rows, bool vec, cudaStream_t s) {
     } else {
       if (sh.nt * sh.ny <= 256) {
         if (sh.nc == 1) return norm_post_kernel<T, YT, V ? 8 : 4, V, 1, 256>;
-        return a.k <= 2 ? norm_post_kernel<T, YT, 2, V, 2, 256> : norm_post_kernel<T, YT, 4, V, 2, 256>;
+        return norm_post_kernel<T, YT, 2, V, 2, 256>;
       }
       return sh.nc == 1 ? norm_post_kernel<T, YT, 4, V, 1, 1024> : norm_post_kernel<T, YT, 2, V, 2, 1024>;
     }

@@ -263,7 +263,7 @@ int dispatch_units(const void* x, int64_t ldx, const int32_t* idx, int T, int E,
 // ------------------------------------------------------------------------------------- combine
 
 template <typename YT, typename OT, bool VEC, int B, int NC>
-__global__ void __launch_bounds__(kRowThreads, VEC && sizeof(YT) == 2 ? 4 : 1)
+__global__ void __launch_bounds__(kRowThreads, VEC && (NC == 2 || sizeof(YT) == 2) ? 4 : 1)
     combine_rows_kernel(const YT* __restrict__ yp, int64_t ldy, const int32_t* __restrict__ inv,
                         const float* __restrict__ wts, int T, int k, int P, int H, OT* __restrict__ out, int64_t ldo) {
   pdl_begin();
@@ -439,21 +439,24 @@ int launch_combine_rows(const void* yp, int64_t ldy, int ydt, const int32_t* inv
                         void* out, int64_t ldo, int odt, cudaStream_t s) {
   if (T == 0) return MOE_OK;
   const bool vec = H % 8 == 0 && rows16(yp, ldy, dtype_size(ydt)) && rows16(out, ldo, dtype_size(odt));
-  // More than four choices: eight at a time, one chunk per thread (2048 tokens of 8 choices, H = 2048:
-  // 34.4 us sort and copy included, 35.5 as two chunks of four). Fewer: two chunks of two or four (8192
-  // tokens of 2, H = 2048: 27 us with four places for two choices, 23 with two). Single values: one
-  // chunk of four. Narrow rows share a block.
-  const bool eight = vec && k > 4, two = vec && !eight && H > 256;
+  // Words: two chunks per thread of two choices at a time (four in 16 bits), in four blocks per SM; one
+  // chunk of eight for more choices in 16 bits (T = 2048, k = 8, H = 2048 with sort and copy: 34.4 us
+  // against 35.5 with two chunks of four and 37.3 of two), and in fp32 for so few tokens that a token's
+  // own latency counts (T = 2048: 18 us against 16 with two chunks of two; T = 1: 1.7 against 4.2).
+  // Single values: one chunk of four. Narrow rows share a block.
+  const bool wide = ydt == MOE_DTYPE_F32;
+  const bool eight = vec && k > 4 && (!wide || T <= 256), two = vec && !eight && H > 256;
   const int nt = row_threads(ceil_div(H, two ? 2 : 1), kRowThreads), ny = kRowThreads / nt;
   const dim3 grid(ceil_div(T, ny), ceil_div(H, 8 * nt * (two ? 2 : 1)));
   note_launch();
   return by_types(ydt, odt, [&](auto* y, auto* o) {
     using YT = std::remove_pointer_t<decltype(y)>;
     using OT = std::remove_pointer_t<decltype(o)>;
-    auto kern = !vec ? combine_rows_kernel<YT, OT, false, 4, 1>
+    auto kern = !vec    ? combine_rows_kernel<YT, OT, false, 4, 1>
                 : eight ? combine_rows_kernel<YT, OT, true, 8, 1>
-                : !two ? combine_rows_kernel<YT, OT, true, 4, 1>
-                : k <= 2 ? combine_rows_kernel<YT, OT, true, 2, 2> : combine_rows_kernel<YT, OT, true, 4, 2>;
+                : !two  ? combine_rows_kernel<YT, OT, true, 4, 1>
+                : k <= 2 ? combine_rows_kernel<YT, OT, true, 2, 2>
+                         : combine_rows_kernel<YT, OT, true, sizeof(YT) == 2 ? 4 : 2, 2>;
     return check_cuda(launch_pdl(kern, grid, dim3(nt, ny), 0, s, static_cast<const YT*>(yp), ldy, inv, wts, T, k, T * k,
                                  H, static_cast<OT*>(out), ldo),
                       "combine_rows_kernel");
