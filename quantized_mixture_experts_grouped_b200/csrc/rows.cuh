@@ -150,13 +150,13 @@ __device__ __forceinline__ void store8(T* row, int c, int nt, int tid, int H, co
   }
 }
 
-// N sums over the block (N = 1, 2, 3, 4 or 8), every thread gets them, in an order fixed by the
+// N sums over the block (N = 1 to 8), every thread gets them, in an order fixed by the
 // block size. The lanes of a warp share the values out between them as they add (half of the values
 // to each half-warp, and so on), so 4 sums cost 6 exchanges and not 20. One barrier per call: `buf`
 // (32 * M floats of shared memory) must not be the buffer of the call before.
 template <int N>
 __device__ __forceinline__ void block_sums(float (&v)[N], float* buf) {
-  constexpr int M = N == 3 ? 4 : N;                 // a fourth value, 0, beside three
+  constexpr int M = N <= 2 ? N : N <= 4 ? 4 : 8;    // zeros beside three, five, six or seven
   constexpr int L = M == 8 ? 3 : M == 4 ? 2 : M == 2 ? 1 : 0, G = 32 >> L;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nw = blockDim.x >> 5;
   float x[M];
