@@ -41,7 +41,8 @@ WIDTHS = [(1, 1), (3, 7), (2, 2048), (5, 1031), (4, 4096), (3, 8192), (2, 12288 
 
 
 # more tokens than blocks at each width, so that a block takes several rows
-LONG = [(5000, 264), (3000, 512), (2500, 72), (1300, 2048), (700, 4096), (500, 8192)]
+LONG = [(5000, 264), (3000, 512), (2500, 72), (1300, 2048), (700, 4096), (500, 8192),
+        (70001, 8)]
 
 
 @pytest.mark.parametrize("T,H", WIDTHS + [(700, 264)] + LONG)
@@ -339,3 +340,30 @@ def test_whole_block_against_autograd(T, drop):
                             ("dw_post", dwp, wp6.grad), ("dw_next", dwn, wn6.grad), ("dgate", dgate, g6.grad)):
         rel = float((got.double() - want).norm() / want.norm())
         assert rel <= 1e-4, (name, rel)
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("H", [512, 4096])
+def test_vectors_on_any_boundary(dt, H):
+    """Weights, gate and the vectors' gradients one element into their buffers; a misaligned gradient
+    beside aligned weights."""
+    g = torch.Generator().manual_seed(H)
+    dt, T = DT[dt], 600
+    y, h = rows(T, H, dt, g, 0, 0.3), rows(T, H, dt, g)
+    odd = lambda m: (torch.randn(H + 1, generator=g) * 0.2 + m).to(dt).cuda()[1:]
+    ho, xn = room(T, H, dt), room(T, H, dt)
+    for vectors in ((odd(1), odd(0.5), odd(1)), tuple(vec(H, dt, g) for _ in range(3))):
+        w, gate, wn = vectors
+        q.moe_norm_post(y, h, ho, EPS, w=w, gate=gate, w_next=wn, x_next=xn)
+        rh, bh, rx, bx = ref.norm_post(y.cpu(), h.cpu(), EPS, 1.0, True, w.cpu(), gate.cpu(), wn.cpu(), True)
+        ref.check(ho, rh, bh, "h_out")
+        ref.check(xn, rx, bx, "x_next")
+        for n in (T, 1):                       # one row: written by the first launch itself
+            dho, dxn, dh, dy = (rows(n, H, dt, g) for _ in range(4))
+            dw, dg, dn = (torch.full((H + 1,), KEEP, device="cuda")[1:] for _ in range(3))
+            q.moe_norm_post_backward(dho, y[:n], dh, dy, EPS, w=w, dw=dw, gate=gate, dgate=dg, h_out=ho[:n], w_next=wn,
+                                     dx_next=dxn, dw_next=dn, ws=ws_for(n, H))
+            want = ref.norm_post_backward(dho.cpu(), y[:n].cpu(), EPS, 1.0, True, w.cpu(), gate.cpu(), ho[:n].cpu(),
+                                          wn.cpu(), dxn.cpu())
+            for name, got in (("dh", dh), ("dy", dy), ("dw", dw), ("dgate", dg), ("dw_next", dn)):
+                ref.check(got, *want[name], name)
