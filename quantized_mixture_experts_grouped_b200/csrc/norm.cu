@@ -285,25 +285,27 @@ __global__ void __launch_bounds__(MAXT, MAXT <= 256 ? 2 : 1) norm_backward_kerne
   }
 }
 
-// Adds the blocks' partial sums: a block has 32 columns (8 lanes of 16 bytes) by 128 runs, run i
-// taking the blocks i, i + 128, ... in order; then the runs are added in a fixed tree. With 19 blocks
-// after one another per run and single values the sums of 592 blocks took 4.5 us.
+// Adds the blocks' partial sums: a block has 4 * L columns (L lanes of 16 bytes) by 1024 / L runs, run i
+// taking the blocks i, i + runs, ... in order; then the runs are added in a fixed tree. A run is at most
+// five blocks long (one turn of loads): with 19 after one another the sums of 592 blocks took 4.5 us.
 struct Sums {
   float* out[kSums];               // the sums asked for, and which of the partial sums each is
   int which[kSums];
 };
+template <int L>
 __global__ void __launch_bounds__(1024) norm_sums_kernel(const float* __restrict__ part, int blocks, int H, int ld,
                                                          const Sums s) {
-  __shared__ float sum[32][33];
+  constexpr int kCols = 4 * L, kRuns = 1024 / L;
+  __shared__ float sum[32][kCols + 1];
   pdl_begin();
   float* out = s.out[blockIdx.y];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, run = threadIdx.x >> 3;
-  const int n = blockIdx.x * 32 + (lane & 7) * 4;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, run = threadIdx.x / L;
+  const int n = blockIdx.x * kCols + (lane & (L - 1)) * 4;
   float v[4] = {0.f, 0.f, 0.f, 0.f};
   if (n < H) {
     const float* p = part + (int64_t)s.which[blockIdx.y] * ld + n;
 #pragma unroll 5
-    for (int b = run; b < blocks; b += 128) {
+    for (int b = run; b < blocks; b += kRuns) {
       const float4 x = *reinterpret_cast<const float4*>(p + (int64_t)b * kSums * ld);
       v[0] += x.x;
       v[1] += x.y;
@@ -313,16 +315,16 @@ __global__ void __launch_bounds__(1024) norm_sums_kernel(const float* __restrict
   }
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    v[i] += __shfl_xor_sync(0xffffffffu, v[i], 8);
-    v[i] += __shfl_xor_sync(0xffffffffu, v[i], 16);
-    if (lane < 8) sum[warp][lane * 4 + i] = v[i];
+#pragma unroll
+    for (int o = L; o < 32; o <<= 1) v[i] += __shfl_xor_sync(0xffffffffu, v[i], o);
+    if (lane < L) sum[warp][lane * 4 + i] = v[i];
   }
   __syncthreads();
-  // warp w adds column w of the 32 warps
-  float total = sum[lane][warp];
+  if (warp >= kCols) return;
+  float total = sum[lane][warp];       // warp w adds column w of the 32 warps
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
-  const int col = blockIdx.x * 32 + warp;
+  const int col = blockIdx.x * kCols + warp;
   if (lane == 0 && col < H) out[col] = total;
 }
 
@@ -511,9 +513,10 @@ int launch_back(const char* me, BackArgs& a, int dtype, bool vec, void* ws, size
     asked.out[n] = sums[i];
     asked.which[n++] = i;
   }
+  const bool many = blocks > 5 * 128;
   note_launch();
-  return check_cuda(launch_pdl(norm_sums_kernel, dim3(ceil_div(a.H, 32), n), dim3(1024), 0, s, (const float*)a.part,
-                               blocks, a.H, a.part_ld, asked),
+  return check_cuda(launch_pdl(many ? norm_sums_kernel<2> : norm_sums_kernel<8>, dim3(ceil_div(a.H, many ? 8 : 32), n),
+                               dim3(1024), 0, s, (const float*)a.part, blocks, a.H, a.part_ld, asked),
                     "norm_sums_kernel");
 }
 

@@ -385,16 +385,19 @@ __global__ void __launch_bounds__(32 * kRouterWarps) route_backward_kernel(const
   if (t >= T) return;
   const int32_t* it = idx + t * k;
   const float *wt = wts + t * k, *dt = dwts + t * k;
-  float mean = 0.f;
-  for (int j = lane; j < k; j += 32) mean = fmaf(wt[j], dt[j], mean);
+  // the first 32 choices in one turn of loads
+  const int e0 = lane < k ? it[lane] : -1;
+  const float w0 = lane < k ? wt[lane] : 0.f, d0 = lane < k ? dt[lane] : 0.f;
+  float mean = w0 * d0;
+  for (int j = lane + 32; j < k; j += 32) mean = fmaf(wt[j], dt[j], mean);
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) mean += __shfl_xor_sync(0xffffffffu, mean, o);
   __syncwarp();
   for (int jb = 0; jb < k; jb += 32) {
     const int j = jb + lane;
-    int e = j < k ? it[j] : -1;
+    int e = jb == 0 ? e0 : j < k ? it[j] : -1;
     if ((unsigned)e >= (unsigned)E) e = -1;
-    const float g = e >= 0 ? wt[j] * (dt[j] - mean) : 0.f;
+    const float g = e < 0 ? 0.f : jb == 0 ? w0 * (d0 - mean) : wt[j] * (dt[j] - mean);
     const unsigned same = __match_any_sync(0xffffffffu, e);
     const int turn = e >= 0 ? __popc(same & ((1u << lane) - 1u)) : 0;
     const int turns = __reduce_max_sync(0xffffffffu, turn);
