@@ -10,6 +10,7 @@
 // All of it moves each row once and does some 10 to 25 flops per value: bound by HBM traffic for
 // large batches, by the latency of one launch for small ones. A block holds its rows in registers
 // (8 or 16 values per thread) between its loads and its stores, so no row is read twice.
+#include <algorithm>
 #include <type_traits>
 
 #include "norm_back.cuh"
@@ -487,8 +488,11 @@ int launch_back(const char* me, BackArgs& a, int dtype, bool vec, void* ws, size
   const int fit = kRingBytes / per_sm / stage_bytes;
   const int stages = fit < kRingStages ? fit : kRingStages;
   const bool use_ring = vec && sh.nc == 1 && sh.nt <= kRingThreads && stages >= 2;
-  // sums over one or two rows take no second launch: one block (two rows of 2048: 2.9 us against 3.7)
-  const int blocks = any && a.T <= 2 ? 1 : back_blocks(a.T, a.H, per_sm);
+  // With sums over the tokens a block is worth its partial sums from two rows on, and eight blocks per
+  // SM are enough (H = 2048, T = 512: 6.7 us against 8.2 with a row each; H = 1024, T = 1000: 6.7 against
+  // 9.7); one or two rows take one block and no second launch (two rows of 2048: 2.9 us against 3.7).
+  int blocks = back_blocks(a.T, a.H, any && per_sm > 8 ? 8 : per_sm);
+  if (any) blocks = a.T <= 2 ? 1 : std::min(blocks, std::max(norm_sms(), ceil_div(a.T, 2)));
   a.part_ld = part_stride(a.H);
   if (any && blocks > 1) {
     const size_t need = norm_ws(a.T, a.H);
