@@ -33,10 +33,10 @@ struct PostArgs {
 };
 
 // The value of one weight or gate vector at this thread's columns (ones where there is none).
-template <bool VEC, typename T>
+template <int NT, typename T>
 __device__ __forceinline__ void weight8(const void* w, int c, int nt, int tid, int H, F2 (&f)[4]) {
   if (w) {
-    load8<VEC>(static_cast<const T*>(w), c, nt, tid, H, f);
+    load8<NT>(static_cast<const T*>(w), c, nt, tid, H, f);
   } else {
 #pragma unroll
     for (int e = 0; e < 4; ++e) f[e] = f2(1.f, 1.f);
@@ -44,11 +44,11 @@ __device__ __forceinline__ void weight8(const void* w, int c, int nt, int tid, i
 }
 
 // The gate of token t at this thread's columns.
-template <bool VEC, typename T>
+template <int NT, typename T>
 __device__ __forceinline__ void gate8(const void* g, int mode, int64_t ld, int64_t t, int c, int nt, int tid, int H,
                                       F2 (&f)[4]) {
   if (mode == MOE_GATE_CHANNEL || mode == MOE_GATE_FULL) {
-    load8<VEC>(static_cast<const T*>(g) + (mode == MOE_GATE_FULL ? t * ld : 0), c, nt, tid, H, f);
+    load8<NT>(static_cast<const T*>(g) + (mode == MOE_GATE_FULL ? t * ld : 0), c, nt, tid, H, f);
   } else {
     const float v = mode == MOE_GATE_TOKEN ? static_cast<const float*>(g)[t] : 1.f;
 #pragma unroll
@@ -72,18 +72,18 @@ __device__ __forceinline__ float squares(const F2 (&v)[NC][4]) {
 // last read as zeros and write nothing.
 constexpr int kBlockRows = 8;
 
-template <typename T, bool VEC, int NC, int MAXT>
+template <typename T, int NT, int NC, int MAXT>
 __global__ void __launch_bounds__(MAXT) norm_pre_kernel(const T* __restrict__ h, int64_t ldh, const T* __restrict__ w,
                                                         float eps, int rows, int H, T* __restrict__ x, int64_t ldx) {
   __shared__ float buf[kBlockRows][32];
   pdl_begin();
   const int64_t t = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
-  const int nt = blockDim.x, tid = threadIdx.x, live = t < rows ? H : 0;
+  const int nt = NT ? NT : blockDim.x, tid = threadIdx.x, live = t < rows ? H : 0;
   F2 v[NC][4], w8[NC][4];
 #pragma unroll
-  for (int c = 0; c < NC; ++c) load8<VEC>(h + t * ldh, c, nt, tid, live, v[c]);
+  for (int c = 0; c < NC; ++c) load8<NT>(h + t * ldh, c, nt, tid, live, v[c]);
 #pragma unroll
-  for (int c = 0; c < NC; ++c) weight8<VEC, T>(w, c, nt, tid, H, w8[c]);
+  for (int c = 0; c < NC; ++c) weight8<NT, T>(w, c, nt, tid, H, w8[c]);
   float ss[1] = {squares(v)};
   block_sums<1>(ss, buf[threadIdx.y]);
   const float r = rsqrtf(ss[0] / H + eps);
@@ -92,35 +92,35 @@ __global__ void __launch_bounds__(MAXT) norm_pre_kernel(const T* __restrict__ h,
   for (int c = 0; c < NC; ++c) {
 #pragma unroll
     for (int e = 0; e < 4; ++e) v[c][e] = mul2(mul2(v[c][e], r2), w8[c][e]);
-    store8<VEC>(x + t * ldx, c, nt, tid, live, v[c]);
+    store8<NT>(x + t * ldx, c, nt, tid, live, v[c]);
   }
 }
 
 // YT: type of the rows y comes from (fused: y is the combine of its token's rows). h_out may be h:
 // a thread reads its values of the row before it writes them, and no other thread reads them.
 // FUSED: the choices read at a time, 0 for rows that are y itself.
-template <typename T, typename YT, int FUSED, bool VEC, int NC, int MAXT>
-__global__ void __launch_bounds__(MAXT, MAXT == 256 && VEC ? (NC == 2 ? 4 : FUSED ? 1 : 8) : 1)
+template <typename T, typename YT, int FUSED, int NT, int NC, int MAXT>
+__global__ void __launch_bounds__(MAXT, MAXT == 256 ? (NC == 2 || NT > 0 ? 4 : FUSED ? 1 : 8) : 1)
     norm_post_kernel(const PostArgs a) {
   __shared__ float buf[2][kBlockRows][32];
   pdl_begin();
   const int64_t t = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
-  const int nt = blockDim.x, tid = threadIdx.x, H = a.H, live = t < a.T ? H : 0;
+  const int nt = NT ? NT : blockDim.x, tid = threadIdx.x, H = a.H, live = t < a.T ? H : 0;
   F2 h[NC][4], y[NC][4], f[4];
   float s[1];
   const T* hrow = static_cast<const T*>(a.h) + t * a.ldh;
 #pragma unroll
-  for (int c = 0; c < NC; ++c) load8<VEC>(hrow, c, nt, tid, live, h[c]);
+  for (int c = 0; c < NC; ++c) load8<NT>(hrow, c, nt, tid, live, h[c]);
   if constexpr (FUSED > 0) {
-    weighted_rows<FUSED, NC, VEC>(static_cast<const YT*>(a.y), a.ldy, a.inv + t * a.k, a.wts + t * a.k, live ? a.k : 0,
+    weighted_rows<FUSED, NC, NT>(static_cast<const YT*>(a.y), a.ldy, a.inv + t * a.k, a.wts + t * a.k, live ? a.k : 0,
                                   a.P, 0, nt, tid, H, y);
     if (a.y_out) {
 #pragma unroll
-      for (int c = 0; c < NC; ++c) store8<VEC>(static_cast<T*>(a.y_out) + t * a.ldyo, c, nt, tid, live, y[c]);
+      for (int c = 0; c < NC; ++c) store8<NT>(static_cast<T*>(a.y_out) + t * a.ldyo, c, nt, tid, live, y[c]);
     }
   } else {
 #pragma unroll
-    for (int c = 0; c < NC; ++c) load8<VEC>(static_cast<const YT*>(a.y) + t * a.ldy, c, nt, tid, live, y[c]);
+    for (int c = 0; c < NC; ++c) load8<NT>(static_cast<const YT*>(a.y) + t * a.ldy, c, nt, tid, live, y[c]);
   }
   if (a.norm_y) {
     s[0] = squares(y);
@@ -129,7 +129,7 @@ __global__ void __launch_bounds__(MAXT, MAXT == 256 && VEC ? (NC == 2 ? 4 : FUSE
     const F2 q2 = f2(q, q);
 #pragma unroll
     for (int c = 0; c < NC; ++c) {
-      weight8<VEC, T>(a.w, c, nt, tid, H, f);
+      weight8<NT, T>(a.w, c, nt, tid, H, f);
 #pragma unroll
       for (int e = 0; e < 4; ++e) y[c][e] = mul2(mul2(y[c][e], q2), f[e]);
     }
@@ -137,10 +137,10 @@ __global__ void __launch_bounds__(MAXT, MAXT == 256 && VEC ? (NC == 2 ? 4 : FUSE
   const F2 alpha = f2(a.alpha, a.alpha);
 #pragma unroll
   for (int c = 0; c < NC; ++c) {
-    gate8<VEC, T>(a.gate, a.gate_mode, a.ldg, live ? t : 0, c, nt, tid, H, f);
+    gate8<NT, T>(a.gate, a.gate_mode, a.ldg, live ? t : 0, c, nt, tid, H, f);
 #pragma unroll
     for (int e = 0; e < 4; ++e) h[c][e] = fma2(alpha, h[c][e], mul2(f[e], y[c][e]));
-    store8<VEC>(static_cast<T*>(a.h_out) + t * a.ldho, c, nt, tid, live, h[c]);
+    store8<NT>(static_cast<T*>(a.h_out) + t * a.ldho, c, nt, tid, live, h[c]);
   }
   if (!a.next) return;
   s[0] = squares(h);
@@ -149,22 +149,22 @@ __global__ void __launch_bounds__(MAXT, MAXT == 256 && VEC ? (NC == 2 ? 4 : FUSE
   const F2 r2 = f2(r, r);
 #pragma unroll
   for (int c = 0; c < NC; ++c) {
-    weight8<VEC, T>(a.w_next, c, nt, tid, H, f);
+    weight8<NT, T>(a.w_next, c, nt, tid, H, f);
 #pragma unroll
     for (int e = 0; e < 4; ++e) h[c][e] = mul2(mul2(h[c][e], r2), f[e]);
-    store8<VEC>(static_cast<T*>(a.x_next) + t * a.ldx, c, nt, tid, live, h[c]);
+    store8<NT>(static_cast<T*>(a.x_next) + t * a.ldx, c, nt, tid, live, h[c]);
   }
 }
 
 // One block takes rows blockIdx.x, + gridDim.x, ...; every thread keeps the same columns, so the
 // sums over the tokens stay in its registers and leave once per block, as partial sums that
 // norm_sums_kernel adds in block order (no atomics: bit-identical run to run).
-template <typename T, bool VEC, int NC, int MAXT>
+template <typename T, int NT, int NC, int MAXT>
 __global__ void __launch_bounds__(MAXT, MAXT <= 256 ? 2 : 1) norm_backward_kernel(const BackArgs a) {
   __shared__ float buf[2][32 * 4];
   int flip = 0;                    // the buffer of the next block-wide sums: never the one of the last
   pdl_begin();
-  const int nt = blockDim.x, tid = threadIdx.x, H = a.H;
+  const int nt = NT ? NT : blockDim.x, tid = threadIdx.x, H = a.H;
   const float inv_h = 1.f / (float)H;
   const F2 zero = f2(0.f, 0.f), alpha = f2(a.alpha, a.alpha);
   F2 sw[NC][4], sg[NC][4], sn[NC][4];
@@ -179,17 +179,17 @@ __global__ void __launch_bounds__(MAXT, MAXT <= 256 ? 2 : 1) norm_backward_kerne
     for (int c = 0; c < NC; ++c) {
 #pragma unroll
       for (int e = 0; e < 4; ++e) d[c][e] = zero;
-      if (a.dho) load8<VEC>(static_cast<const T*>(a.dho) + t * a.lddho, c, nt, tid, H, d[c]);
-      if (a.has_y) load8<VEC>(static_cast<const T*>(a.y) + t * a.ldy, c, nt, tid, H, y[c]);
+      if (a.dho) load8<NT>(static_cast<const T*>(a.dho) + t * a.lddho, c, nt, tid, H, d[c]);
+      if (a.has_y) load8<NT>(static_cast<const T*>(a.y) + t * a.ldy, c, nt, tid, H, y[c]);
       if (a.next) {
-        load8<VEC>(static_cast<const T*>(a.ho) + t * a.ldho, c, nt, tid, H, h[c]);
-        load8<VEC>(static_cast<const T*>(a.dx) + t * a.lddx, c, nt, tid, H, x[c]);
+        load8<NT>(static_cast<const T*>(a.ho) + t * a.ldho, c, nt, tid, H, h[c]);
+        load8<NT>(static_cast<const T*>(a.dx) + t * a.lddx, c, nt, tid, H, x[c]);
       }
     }
 #pragma unroll
     for (int c = 0; c < NC; ++c) {
       if (a.next) {
-        weight8<VEC, T>(a.w_next, c, nt, tid, H, f);
+        weight8<NT, T>(a.w_next, c, nt, tid, H, f);
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           p0 = fma2(h[c][e], h[c][e], p0);
@@ -212,7 +212,7 @@ __global__ void __launch_bounds__(MAXT, MAXT <= 256 ? 2 : 1) norm_backward_kerne
       const F2 r2 = f2(r, r), m2 = f2(m, m);
 #pragma unroll
       for (int c = 0; c < NC; ++c) {
-        weight8<VEC, T>(a.w_next, c, nt, tid, H, f);
+        weight8<NT, T>(a.w_next, c, nt, tid, H, f);
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           const F2 n = mul2(h[c][e], r2);
@@ -226,7 +226,7 @@ __global__ void __launch_bounds__(MAXT, MAXT <= 256 ? 2 : 1) norm_backward_kerne
     for (int c = 0; c < NC; ++c) {
 #pragma unroll
       for (int e = 0; e < 4; ++e) f[e] = mul2(alpha, d[c][e]);
-      store8<VEC>(static_cast<T*>(a.dh) + t * a.lddh, c, nt, tid, H, f);
+      store8<NT>(static_cast<T*>(a.dh) + t * a.lddh, c, nt, tid, H, f);
     }
     if (!a.has_y) continue;
     const float q = a.norm_y ? rsqrtf(s[2] * inv_h + a.eps) : 1.f;
@@ -235,8 +235,8 @@ __global__ void __launch_bounds__(MAXT, MAXT <= 256 ? 2 : 1) norm_backward_kerne
 #pragma unroll
     for (int c = 0; c < NC; ++c) {
       F2 g[4], u[4];
-      weight8<VEC, T>(a.norm_y ? a.w : nullptr, c, nt, tid, H, f);
-      gate8<VEC, T>(a.gate, a.gate_mode, a.ldg, t, c, nt, tid, H, g);
+      weight8<NT, T>(a.norm_y ? a.w : nullptr, c, nt, tid, H, f);
+      gate8<NT, T>(a.gate, a.gate_mode, a.ldg, t, c, nt, tid, H, g);
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         y[c][e] = mul2(y[c][e], q2);
@@ -249,7 +249,7 @@ __global__ void __launch_bounds__(MAXT, MAXT <= 256 ? 2 : 1) norm_backward_kerne
         z0 = fma2(d[c][e], y[c][e], z0);
       }
       if (a.gate_mode == MOE_GATE_FULL && a.dgate)
-        store8<VEC>(static_cast<T*>(a.dgate) + t * a.lddg, c, nt, tid, H, u);
+        store8<NT>(static_cast<T*>(a.dgate) + t * a.lddg, c, nt, tid, H, u);
     }
     float z[2] = {sum_of(z0), sum_of(z1)};
     if (a.norm_y || a.gate_mode == MOE_GATE_TOKEN) {
@@ -265,7 +265,7 @@ __global__ void __launch_bounds__(MAXT, MAXT <= 256 ? 2 : 1) norm_backward_kerne
 #pragma unroll
         for (int e = 0; e < 4; ++e) d[c][e] = mul2(q2, fma2(y[c][e], m2, d[c][e]));
       }
-      store8<VEC>(static_cast<T*>(a.dy) + t * a.lddy, c, nt, tid, H, d[c]);
+      store8<NT>(static_cast<T*>(a.dy) + t * a.lddy, c, nt, tid, H, d[c]);
     }
   }
   float* out[kSums] = {a.dw, a.gate_mode == MOE_GATE_CHANNEL ? static_cast<float*>(a.dgate) : nullptr, a.dw_next};
@@ -279,7 +279,7 @@ __global__ void __launch_bounds__(MAXT, MAXT <= 256 ? 2 : 1) norm_backward_kerne
       from_pairs(i == 0 ? sw[c] : i == 1 ? sg[c] : sn[c], v);
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        const int n = col_of<VEC>(c, e, nt, tid);
+        const int n = col_of<NT>(c, e, nt, tid);
         if (n < H) o[n] = v.v[e];
       }
     }
@@ -335,8 +335,13 @@ __global__ void __launch_bounds__(1024) norm_sums_kernel(const float* __restrict
 struct Shape {
   int nt, nc, ny;
 };
-// Backward: one row at a time, one chunk up to 8192 values.
-Shape shape_of(int H) {
+// Backward: one row at a time, one chunk up to 8192 values (`words`: rows of 16-byte words; single values
+// take one of the block sizes that are built).
+Shape shape_of(int H, bool words) {
+  if (!words) {
+    const int nt = H <= 256 ? 32 : H <= 1024 ? 128 : H <= 2048 ? 256 : H <= 4096 ? 512 : 1024;
+    return {nt, H <= 8 * nt ? 1 : 2, 1};
+  }
   const int nt = row_threads(H, 1024);
   if (H <= 8 * nt) return {nt, 1, 1};
   return {row_threads(ceil_div(H, 2), 1024), 2, 1};
@@ -344,11 +349,26 @@ Shape shape_of(int H) {
 // Forward, up to 4096 values: 256 threads, with two chunks per thread (half as many exchanges per row,
 // twice the loads in flight per thread: T = 2048, H = 2048, bf16, post with next norm 6.2 us against
 // 7.1), but one up to 256 rows of 2048 values, where a row's own latency counts (2.2 against 2.4 at
-// T = 1). Wider rows take more threads.
-Shape shape_forward(int rows, int H) {
-  if (H > 4096) return shape_of(H);
+// T = 1). Wider rows take more threads. Single values: two chunks from 1025 on.
+Shape shape_forward(int rows, int H, bool words) {
+  if (!words) {
+    const int nc = H <= 1024 ? 1 : 2, nt = H <= 256 ? 32 : H <= 2048 ? 128 : H <= 4096 ? 256 : 1024;
+    return {nt, nc, nt > 256 ? 1 : 256 / nt};
+  }
+  if (H > 4096) return shape_of(H, true);
   const int nc = H <= 256 || (H <= 2048 && rows <= 256) ? 1 : 2, nt = row_threads(ceil_div(H, nc), 256);
   return {nt, nc, 256 / nt < kBlockRows ? 256 / nt : kBlockRows};
+}
+// Calls f(threads, chunks) as integral constants for the forward shape of single values.
+template <typename F>
+auto by_values(const Shape& sh, F f) {
+  using One = std::integral_constant<int, 1>;
+  using Two = std::integral_constant<int, 2>;
+  if (sh.nt == 32) return f(std::integral_constant<int, 32>(), One());
+  if (sh.nt == 128 && sh.nc == 1) return f(std::integral_constant<int, 128>(), One());
+  if (sh.nt == 128) return f(std::integral_constant<int, 128>(), Two());
+  if (sh.nt == 256) return f(std::integral_constant<int, 256>(), Two());
+  return f(std::integral_constant<int, 1024>(), Two());
 }
 
 // Calls f(typed null pointer) for the row type.
@@ -411,25 +431,21 @@ bool gate16(const void* gate, int mode, int64_t ld, size_t z) {
 
 template <typename T, typename YT, bool FUSED>
 int launch_post(const PostArgs& a, int rows, bool vec, cudaStream_t s) {
-  const Shape sh = shape_forward(rows, a.H);
+  const Shape sh = shape_forward(rows, a.H, vec);
   // choices read at a time: eight with one chunk per thread, for few tokens; two with two chunks, which
   // leaves room for four blocks per SM (T = 2048, k = 8, H = 2048, bf16: 17.2 us, with four at a time in
   // two blocks 22.3, and moe_combine and moe_norm_post one after the other 20.3)
-  auto pick = [&](auto vec_) {
-    constexpr bool V = decltype(vec_)::value;
-    if constexpr (!FUSED) {
-      if (sh.nt * sh.ny <= 256)
-        return sh.nc == 1 ? norm_post_kernel<T, YT, 0, V, 1, 256> : norm_post_kernel<T, YT, 0, V, 2, 256>;
-      return sh.nc == 1 ? norm_post_kernel<T, YT, 0, V, 1, 1024> : norm_post_kernel<T, YT, 0, V, 2, 1024>;
-    } else {
-      if (sh.nt * sh.ny <= 256) {
-        if (sh.nc == 1) return norm_post_kernel<T, YT, V ? 8 : 4, V, 1, 256>;
-        return norm_post_kernel<T, YT, 2, V, 2, 256>;
-      }
-      return sh.nc == 1 ? norm_post_kernel<T, YT, 4, V, 1, 1024> : norm_post_kernel<T, YT, 2, V, 2, 1024>;
-    }
+  constexpr int F8 = FUSED ? 8 : 0, F4 = FUSED ? 4 : 0, F2_ = FUSED ? 2 : 0;
+  auto words = [&]() {
+    if (sh.nt * sh.ny <= 256)
+      return sh.nc == 1 ? norm_post_kernel<T, YT, F8, 0, 1, 256> : norm_post_kernel<T, YT, F2_, 0, 2, 256>;
+    return sh.nc == 1 ? norm_post_kernel<T, YT, F4, 0, 1, 1024> : norm_post_kernel<T, YT, F2_, 0, 2, 1024>;
   };
-  auto kern = vec ? pick(std::true_type()) : pick(std::false_type());
+  auto values = [](auto n, auto c) {
+    constexpr int N = decltype(n)::value, C = decltype(c)::value;
+    return norm_post_kernel<T, YT, C == 1 ? F4 : F2_, N, C, N <= 256 ? 256 : N>;
+  };
+  auto kern = vec ? words() : by_values(sh, values);
   note_launch();
   return check_cuda(launch_pdl(kern, dim3(ceil_div(rows, sh.ny)), dim3(sh.nt, sh.ny), 0, s, a), "norm_post_kernel");
 }
@@ -457,14 +473,14 @@ int check_post(const char* me, const PostArgs& a, int T, int H, int dtype, int f
 
 // The kernel built for a block of this size: the fewer threads, the more registers each has. Rows of
 // 16-byte words come here only when they are too wide for the ring.
-template <typename T, bool VEC>
-auto back_kernel(Shape sh) {
-  if (sh.nc == 2) return norm_backward_kernel<T, VEC, 2, 1024>;
-  if constexpr (!VEC) {
-    if (sh.nt <= 256) return norm_backward_kernel<T, VEC, 1, 256>;
-    if (sh.nt <= 512) return norm_backward_kernel<T, VEC, 1, 512>;
-  }
-  return norm_backward_kernel<T, VEC, 1, 1024>;
+template <typename T>
+auto back_kernel(const Shape& sh, bool words) {
+  if (words) return sh.nc == 2 ? norm_backward_kernel<T, 0, 2, 1024> : norm_backward_kernel<T, 0, 1, 1024>;
+  if (sh.nc == 2) return norm_backward_kernel<T, 1024, 2, 1024>;
+  return by_width<32, 128, 256, 512, 1024>(8 * sh.nt, [](auto n) {
+    constexpr int N = decltype(n)::value;
+    return norm_backward_kernel<T, N, 1, N <= 256 ? 256 : N>;
+  });
 }
 
 int launch_back(const char* me, BackArgs& a, int dtype, bool vec, void* ws, size_t ws_bytes, cudaStream_t s) {
@@ -477,7 +493,7 @@ int launch_back(const char* me, BackArgs& a, int dtype, bool vec, void* ws, size
         if (int rc = check_cuda(cudaMemsetAsync(p, 0, sizeof(float) * a.H, s), me)) return rc;
     return MOE_OK;
   }
-  const Shape sh = shape_of(a.H);
+  const Shape sh = shape_of(a.H, vec);
   // the ring wants three stages (two rows ahead) and takes up to four; fewer blocks share an SM where
   // that needs their shared memory. Two always fit: five fp32 tensors of 512 * 8 values are 80 KB.
   const int tensors = (a.dho ? 1 : 0) + (a.has_y ? 1 : 0) + (a.next ? 2 : 0) + (a.gate_mode == MOE_GATE_FULL ? 1 : 0);
@@ -506,8 +522,7 @@ int launch_back(const char* me, BackArgs& a, int dtype, bool vec, void* ws, size
   int rc = by_type(dtype, [&](auto* p) {
     using T = std::remove_pointer_t<decltype(p)>;
     if (use_ring) return launch_norm_ring<T>(a, blocks, sh.nt, stages, stage_bytes, s);
-    auto kern = vec ? back_kernel<T, true>(sh) : back_kernel<T, false>(sh);
-    return check_cuda(launch_pdl(kern, dim3(blocks), dim3(sh.nt), 0, s, a), "norm_backward_kernel");
+    return check_cuda(launch_pdl(back_kernel<T>(sh, vec), dim3(blocks), dim3(sh.nt), 0, s, a), "norm_backward_kernel");
   });
   if (rc || !any || blocks == 1) return rc;
   Sums asked{};
@@ -548,16 +563,19 @@ MOE_API int moe_norm_pre(const void* h, int64_t h_stride, int dtype, const void*
   if (T == 0) return MOE_OK;
   const size_t z = dtype_size(dtype);
   const bool vec = H % 8 == 0 && rows16(h, h_stride, z) && rows16(x, x_stride, z) && rows16(w, 0, z);
-  const Shape sh = shape_forward(T, H);
+  const Shape sh = shape_forward(T, H, vec);
   note_launch();
   return by_type(dtype, [&](auto* p) {
     using T_ = std::remove_pointer_t<decltype(p)>;
-    auto pick = [&](auto vec_) {
-      constexpr bool V = decltype(vec_)::value;
-      if (sh.nt * sh.ny <= 256) return sh.nc == 1 ? norm_pre_kernel<T_, V, 1, 256> : norm_pre_kernel<T_, V, 2, 256>;
-      return sh.nc == 1 ? norm_pre_kernel<T_, V, 1, 1024> : norm_pre_kernel<T_, V, 2, 1024>;
+    auto words = [&]() {
+      if (sh.nt * sh.ny <= 256) return sh.nc == 1 ? norm_pre_kernel<T_, 0, 1, 256> : norm_pre_kernel<T_, 0, 2, 256>;
+      return sh.nc == 1 ? norm_pre_kernel<T_, 0, 1, 1024> : norm_pre_kernel<T_, 0, 2, 1024>;
     };
-    auto kern = vec ? pick(std::true_type()) : pick(std::false_type());
+    auto values = [](auto n, auto c) {
+      constexpr int N = decltype(n)::value;
+      return norm_pre_kernel<T_, N, decltype(c)::value, N <= 256 ? 256 : N>;
+    };
+    auto kern = vec ? words() : by_values(sh, values);
     return check_cuda(launch_pdl(kern, dim3(ceil_div(T, sh.ny)), dim3(sh.nt, sh.ny), 0,
                                  reinterpret_cast<cudaStream_t>(stream), static_cast<const T_*>(h), h_stride,
                                  static_cast<const T_*>(w), eps, T, H, static_cast<T_*>(x), x_stride),

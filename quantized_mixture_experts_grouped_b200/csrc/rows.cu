@@ -262,18 +262,18 @@ int dispatch_units(const void* x, int64_t ldx, const int32_t* idx, int T, int E,
 
 // ------------------------------------------------------------------------------------- combine
 
-template <typename YT, typename OT, bool VEC, int B, int NC>
-__global__ void __launch_bounds__(kRowThreads, VEC && (NC == 2 || sizeof(YT) == 2) ? 4 : 1)
+template <typename YT, typename OT, int NT, int B, int NC>
+__global__ void __launch_bounds__(kRowThreads, NC == 2 || sizeof(YT) == 2 || NT > 0 ? 4 : 1)
     combine_rows_kernel(const YT* __restrict__ yp, int64_t ldy, const int32_t* __restrict__ inv,
                         const float* __restrict__ wts, int T, int k, int P, int H, OT* __restrict__ out, int64_t ldo) {
   pdl_begin();
   const int64_t t = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
   if (t >= T) return;
   F2 v[NC][4];
-  weighted_rows<B, NC, VEC>(yp, ldy, inv + t * k, wts ? wts + t * k : nullptr, k, P, blockIdx.y * NC, blockDim.x,
+  weighted_rows<B, NC, NT>(yp, ldy, inv + t * k, wts ? wts + t * k : nullptr, k, P, blockIdx.y * NC, blockDim.x,
                             threadIdx.x, H, v);
 #pragma unroll
-  for (int c = 0; c < NC; ++c) store8<VEC>(out + t * ldo, blockIdx.y * NC + c, blockDim.x, threadIdx.x, H, v[c]);
+  for (int c = 0; c < NC; ++c) store8<NT>(out + t * ldo, blockIdx.y * NC + c, blockDim.x, threadIdx.x, H, v[c]);
 }
 
 // Gradient of combine: one block per token. dout's row stays in registers while the token's rows
@@ -281,15 +281,15 @@ __global__ void __launch_bounds__(kRowThreads, VEC && (NC == 2 || sizeof(YT) == 
 // dot products of up to kDots choices are reduced together at the end of the row.
 constexpr int kDots = 8;
 
-template <typename YT, typename OT, bool VEC>
-__global__ void __launch_bounds__(kRowThreads, VEC ? 4 : 2)
+template <typename YT, typename OT, int NT>
+__global__ void __launch_bounds__(kRowThreads, 4)
     combine_backward_kernel(const OT* __restrict__ dout, int64_t ldo, const YT* __restrict__ yp, int64_t ldy,
                             const int32_t* __restrict__ inv, const float* __restrict__ wts, int k, int P, int H,
                             YT* __restrict__ dyp, int64_t lddy, float* __restrict__ dwts) {
   __shared__ float buf[2][32 * kDots];
   pdl_begin();
   const int64_t t = blockIdx.x;
-  const int nt = blockDim.x, tid = threadIdx.x;
+  const int nt = NT ? NT : blockDim.x, tid = threadIdx.x;
   const int chunks = (H + 8 * nt - 1) / (8 * nt);
   const int32_t* it = inv + t * k;
   const float* wt = wts + t * k;
@@ -311,7 +311,7 @@ __global__ void __launch_bounds__(kRowThreads, VEC ? 4 : 2)
     for (int b = 0; b < kDots; ++b) part[b] = f2(0.f, 0.f);
     for (int c = 0; c < chunks; ++c) {
       F2 d[4];
-      load8<VEC>(dout + t * ldo, c, nt, tid, H, d);
+      load8<NT>(dout + t * ldo, c, nt, tid, H, d);
       // four choices' words at a time and four blocks per SM: T = 2048, k = 8, H = 2048 took 54 us for
       // the whole gradient with eight and three, 49 with four and five (spills), 44 like this
       constexpr int B = 4;
@@ -323,7 +323,7 @@ __global__ void __launch_bounds__(kRowThreads, VEC ? 4 : 2)
 #pragma unroll
           for (int b = 0; b < B; ++b) {
             const bool on = pos[b0 + b] >= 0;
-            r[b] = load_raw<VEC>(yp + (int64_t)(on ? pos[b0 + b] : 0) * ldy, c, nt, tid, on ? H : 0);
+            r[b] = load_raw<NT>(yp + (int64_t)(on ? pos[b0 + b] : 0) * ldy, c, nt, tid, on ? H : 0);
           }
         }
         if (dyp) {          // does not wait for yp's rows
@@ -335,7 +335,7 @@ __global__ void __launch_bounds__(kRowThreads, VEC ? 4 : 2)
 #pragma unroll
             for (int e = 0; e < 4; ++e) g[e] = mul2(w2, d[e]);
             const bool on = pos[b0 + b] >= 0;
-            store8<VEC>(dyp + (int64_t)(on ? pos[b0 + b] : 0) * lddy, c, nt, tid, on ? H : 0, g);
+            store8<NT>(dyp + (int64_t)(on ? pos[b0 + b] : 0) * lddy, c, nt, tid, on ? H : 0, g);
           }
         }
         if (dwts) {
@@ -343,7 +343,7 @@ __global__ void __launch_bounds__(kRowThreads, VEC ? 4 : 2)
           for (int b = 0; b < B; ++b) {
             if (j0 + b0 + b >= k) break;
             F2 v[4];
-            to_pairs(r[b], v);
+            raw_pairs<NT>(r[b], v);
 #pragma unroll
             for (int e = 0; e < 4; ++e) part[b0 + b] = fma2(d[e], v[e], part[b0 + b]);
           }
@@ -438,6 +438,9 @@ int by_types(int y, int o, F f) {
   return fail(MOE_ERR_ARG, "unsupported types: rows %d with results %d", y, o);
 }
 
+// Threads of a block for rows moved value by value, as by_width<32, 128, 256> chooses.
+int value_threads(int H) { return H <= 256 ? 32 : H <= 1024 ? 128 : kRowThreads; }
+
 int launch_combine_rows(const void* yp, int64_t ldy, int ydt, const int32_t* inv, const float* wts, int T, int H, int k,
                         void* out, int64_t ldo, int odt, cudaStream_t s) {
   if (T == 0) return MOE_OK;
@@ -449,17 +452,17 @@ int launch_combine_rows(const void* yp, int64_t ldy, int ydt, const int32_t* inv
   // Single values: one chunk of four. Narrow rows share a block.
   const bool wide = ydt == MOE_DTYPE_F32;
   const bool eight = vec && k > 4 && (!wide || T <= 256), two = vec && !eight && H > 256;
-  const int nt = row_threads(ceil_div(H, two ? 2 : 1), kRowThreads), ny = kRowThreads / nt;
+  const int nt = vec ? row_threads(ceil_div(H, two ? 2 : 1), kRowThreads) : value_threads(H), ny = kRowThreads / nt;
   const dim3 grid(ceil_div(T, ny), ceil_div(H, 8 * nt * (two ? 2 : 1)));
   note_launch();
   return by_types(ydt, odt, [&](auto* y, auto* o) {
     using YT = std::remove_pointer_t<decltype(y)>;
     using OT = std::remove_pointer_t<decltype(o)>;
-    auto kern = !vec    ? combine_rows_kernel<YT, OT, false, 4, 1>
-                : eight ? combine_rows_kernel<YT, OT, true, 8, 1>
-                : !two  ? combine_rows_kernel<YT, OT, true, 4, 1>
-                : k <= 2 ? combine_rows_kernel<YT, OT, true, 2, 2>
-                         : combine_rows_kernel<YT, OT, true, sizeof(YT) == 2 ? 4 : 2, 2>;
+    auto kern = !vec    ? by_width<32, 128, 256>(H, [](auto n) { return combine_rows_kernel<YT, OT, decltype(n)::value, 4, 1>; })
+                : eight ? combine_rows_kernel<YT, OT, 0, 8, 1>
+                : !two  ? combine_rows_kernel<YT, OT, 0, 4, 1>
+                : k <= 2 ? combine_rows_kernel<YT, OT, 0, 2, 2>
+                         : combine_rows_kernel<YT, OT, 0, sizeof(YT) == 2 ? 4 : 2, 2>;
     return check_cuda(launch_pdl(kern, grid, dim3(nt, ny), 0, s, static_cast<const YT*>(yp), ldy, inv, wts, T, k, T * k,
                                  H, static_cast<OT*>(out), ldo),
                       "combine_rows_kernel");
@@ -570,8 +573,9 @@ MOE_API int moe_combine_backward(const void* dout, int64_t dout_stride, int dout
   return by_types(yp_dtype, dout_dtype, [&](auto* y, auto* o) {
     using YT = std::remove_pointer_t<decltype(y)>;
     using OT = std::remove_pointer_t<decltype(o)>;
-    auto kern = vec ? combine_backward_kernel<YT, OT, true> : combine_backward_kernel<YT, OT, false>;
-    return check_cuda(launch_pdl(kern, dim3(T), dim3(row_threads(H, kRowThreads)), 0,
+    auto kern = vec ? combine_backward_kernel<YT, OT, 0>
+                    : by_width<32, 128, 256>(H, [](auto n) { return combine_backward_kernel<YT, OT, decltype(n)::value>; });
+    return check_cuda(launch_pdl(kern, dim3(T), dim3(vec ? row_threads(H, kRowThreads) : value_threads(H)), 0,
                                  reinterpret_cast<cudaStream_t>(stream), static_cast<const OT*>(dout), dout_stride,
                                  static_cast<const YT*>(yp), yp_stride, inv, wts, k, T * k, H, static_cast<YT*>(dyp),
                                  dyp_stride, dwts),

@@ -1,13 +1,17 @@
 // Rows of bf16, fp16 or fp32 values read and written by the row operators (rows.cu, norm.cu).
 //
-// A block of nt threads covers a row of H values in chunks of 8 values per thread, held as fp32.
-// VEC: thread i owns the 8 consecutive values from (c * nt + i) * 8, moved as 16-byte words; it
-// needs H a multiple of 8 and every row to start on a 16-byte boundary. Otherwise thread i owns
-// the values (8 * c + e) * nt + i (e = 0..7): single values, neighbouring threads on neighbouring
-// addresses, any H and any stride. Values past H read as 0 and are not written.
+// A block of nt threads covers a row of H values in chunks of 8 values per thread, held as fp32. NT, a
+// template argument of everything below, is 0 for rows of 16-byte words: thread i owns the 8
+// consecutive values from (c * nt + i) * 8; it needs H a multiple of 8 and every row to start on a
+// 16-byte boundary. Otherwise NT is nt itself, and thread i owns the values (8 * c + e) * NT + i
+// (e = 0..7): single values, neighbouring threads on neighbouring addresses, any H and any stride. (As a
+// constant it makes the addresses of a row's values offsets of one pointer: 2 to 4 instructions per
+// value read, not 20.) Values past H read as 0 and are not written.
 #pragma once
 
 #include <cuda_fp16.h>
+
+#include <type_traits>
 
 #include "common.cuh"
 
@@ -30,25 +34,29 @@ template <> struct RowType<float> {
 template <typename T> struct alignas(16) Raw8 { T v[8]; };
 
 // Index of value e of chunk c of thread tid.
-template <bool VEC>
+template <int NT>
 __device__ __forceinline__ int col_of(int c, int e, int nt, int tid) {
-  return VEC ? (c * nt + tid) * 8 + e : (c * 8 + e) * nt + tid;
+  return NT == 0 ? (c * nt + tid) * 8 + e : (c * 8 + e) * NT + tid;
 }
 
-template <bool VEC, typename T>
+template <int NT, typename T>
 __device__ __forceinline__ Raw8<T> load_raw(const T* row, int c, int nt, int tid, int H) {
   Raw8<T> r;
-  if (VEC) {
-    const int n0 = col_of<true>(c, 0, nt, tid);
+  if (NT == 0) {
+    const int n0 = col_of<0>(c, 0, nt, tid);
     uint4* q = reinterpret_cast<uint4*>(&r);
 #pragma unroll
     for (int i = 0; i < (int)sizeof(T) / 2; ++i)
       q[i] = n0 < H ? reinterpret_cast<const uint4*>(row + n0)[i] : make_uint4(0, 0, 0, 0);
   } else {
+    const T* p = row + (c * 8 * NT + tid);
+    if ((c * 8 + 8) * NT <= H) {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const int n = col_of<false>(c, e, nt, tid);
-      r.v[e] = n < H ? row[n] : RowType<T>::from(0.f);
+      for (int e = 0; e < 8; ++e) r.v[e] = p[e * NT];
+    } else {
+      const int left = H - c * 8 * NT - tid;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) r.v[e] = e * NT < left ? p[e * NT] : RowType<T>::from(0.f);
     }
   }
   return r;
@@ -122,9 +130,20 @@ __device__ __forceinline__ void from_pairs(const F2 (&f)[4], Raw8<float>& r) {
   }
 }
 
-template <bool VEC, typename T>
+// The eight values as pairs: of packed words, or value by value.
+template <int NT, typename T>
+__device__ __forceinline__ void raw_pairs(const Raw8<T>& r, F2 (&f)[4]) {
+  if (NT == 0) {
+    to_pairs(r, f);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) f[i] = f2(RowType<T>::to(r.v[2 * i]), RowType<T>::to(r.v[2 * i + 1]));
+  }
+}
+
+template <int NT, typename T>
 __device__ __forceinline__ void load8(const T* row, int c, int nt, int tid, int H, F2 (&f)[4]) {
-  to_pairs(load_raw<VEC>(row, c, nt, tid, H), f);
+  raw_pairs<NT>(load_raw<NT>(row, c, nt, tid, H), f);
 }
 
 template <typename T>
@@ -135,17 +154,29 @@ __device__ __forceinline__ void store_raw(T* row, int n0, int H, const Raw8<T>& 
   for (int i = 0; i < (int)sizeof(T) / 2; ++i) reinterpret_cast<uint4*>(row + n0)[i] = q[i];
 }
 
-template <bool VEC, typename T>
+template <int NT, typename T>
 __device__ __forceinline__ void store8(T* row, int c, int nt, int tid, int H, const F2 (&f)[4]) {
-  Raw8<T> r;
-  from_pairs(f, r);
-  if (VEC) {
-    store_raw(row, col_of<true>(c, 0, nt, tid), H, r);
+  if (NT == 0) {
+    Raw8<T> r;
+    from_pairs(f, r);
+    store_raw(row, col_of<0>(c, 0, nt, tid), H, r);
   } else {
+    T* p = row + (c * 8 * NT + tid);
+    const int left = (c * 8 + 8) * NT <= H ? 8 * NT : H - c * 8 * NT - tid;
+    if (left == 8 * NT) {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const int n = col_of<false>(c, e, nt, tid);
-      if (n < H) row[n] = r.v[e];
+      for (int i = 0; i < 4; ++i) {
+        const float2 v = halves(f[i]);
+        p[2 * i * NT] = RowType<T>::from(v.x);
+        p[(2 * i + 1) * NT] = RowType<T>::from(v.y);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float2 v = halves(f[i]);
+        if (2 * i * NT < left) p[2 * i * NT] = RowType<T>::from(v.x);
+        if ((2 * i + 1) * NT < left) p[(2 * i + 1) * NT] = RowType<T>::from(v.y);
+      }
     }
   }
 }
@@ -203,7 +234,7 @@ __device__ __forceinline__ void block_sums(float (&v)[N], float* buf) {
 // first of their rows, and the rows before the first is used, so that one token waits for memory
 // twice and not twice per choice (2048 tokens, 8 choices, H = 2048: 44 us when each row waited for
 // its own place).
-template <int B, int NC, bool VEC, typename T>
+template <int B, int NC, int NT, typename T>
 __device__ __forceinline__ void weighted_rows(const T* rows, int64_t ld, const int32_t* inv, const float* wts, int k,
                                               int P, int c0, int nt, int tid, int H, F2 (&out)[NC][4]) {
 #pragma unroll
@@ -227,7 +258,7 @@ __device__ __forceinline__ void weighted_rows(const T* rows, int64_t ld, const i
       w[b] = on ? w[b] : 0.f;
       const T* row = rows + (int64_t)(on ? p[b] : 0) * ld;
 #pragma unroll
-      for (int c = 0; c < NC; ++c) r[b][c] = load_raw<VEC>(row, c0 + c, nt, tid, on ? H : 0);
+      for (int c = 0; c < NC; ++c) r[b][c] = load_raw<NT>(row, c0 + c, nt, tid, on ? H : 0);
     }
 #pragma unroll
     for (int b = 0; b < B; ++b) {
@@ -236,7 +267,7 @@ __device__ __forceinline__ void weighted_rows(const T* rows, int64_t ld, const i
 #pragma unroll
       for (int c = 0; c < NC; ++c) {
         F2 v[4];
-        to_pairs(r[b][c], v);
+        raw_pairs<NT>(r[b][c], v);
 #pragma unroll
         for (int e = 0; e < 4; ++e) out[c][e] = fma2(w2, v[e], out[c][e]);
       }
@@ -256,6 +287,16 @@ inline size_t dtype_size(int dtype) {
 // Whether rows of `stride` elements from `p` all start on a 16-byte boundary (null: nothing to move).
 inline bool rows16(const void* p, int64_t stride, size_t size) {
   return !p || ((reinterpret_cast<uintptr_t>(p) | (uintptr_t)(stride * (int64_t)size)) & 15) == 0;
+}
+// Calls f(integral constant) for the block size of single values, among those given (ascending), whose
+// one chunk covers H, or else the last.
+template <int N, int... Rest, typename F>
+auto by_width(int H, F f) {
+  if constexpr (sizeof...(Rest) == 0) {
+    return f(std::integral_constant<int, N>());
+  } else {
+    return H <= 8 * N ? f(std::integral_constant<int, N>()) : by_width<Rest...>(H, f);
+  }
 }
 // Threads of a block that covers H values in chunks of 8, at most `most`.
 inline int row_threads(int H, int most) {
