@@ -165,6 +165,33 @@ __device__ __forceinline__ void copy_row(const U* __restrict__ src, U* xp, int64
   }
 }
 
+// 16-bit values on any boundary: a thread takes the values c - 1, c, c + 1 (c even) and writes whole
+// 32-bit words, the pair (c, c + 1) where the place starts on one and (c - 1, c) where it does not (a
+// value at a time: 26 us against 12 for 2048 tokens of 8 choices in words).
+template <>
+__device__ __forceinline__ void copy_row<uint16_t>(const uint16_t* __restrict__ src, uint16_t* xp, int64_t ldp,
+                                                   const int32_t* place, int k, int n) {
+  for (int c = 2 * threadIdx.x; c <= n; c += 2 * blockDim.x) {
+    const uint32_t before = c > 0 ? src[c - 1] : 0, here = c < n ? src[c] : 0, after = c + 1 < n ? src[c + 1] : 0;
+    const uint32_t even = here | after << 16, odd = before | here << 16;
+    for (int j = 0; j < k; ++j) {
+      const int p = place[j];
+      if (p < 0) continue;
+      uint16_t* dst = xp + (int64_t)p * ldp + c;
+      if ((reinterpret_cast<uintptr_t>(dst) & 3) == 0) {
+        if (c + 1 < n) *reinterpret_cast<uint32_t*>(dst) = even;
+        else if (c < n) *dst = (uint16_t)here;
+      } else if (c > 0 && c < n) {
+        *reinterpret_cast<uint32_t*>(dst - 1) = odd;
+      } else if (c == 0) {
+        *dst = (uint16_t)here;
+      } else {
+        dst[-1] = (uint16_t)before;
+      }
+    }
+  }
+}
+
 template <typename U>
 __global__ void __launch_bounds__(kRowThreads) copy_rows_kernel(const U* __restrict__ x, int64_t ldx,
                                                                 const int32_t* __restrict__ inv, int k, int n, U* xp,
