@@ -159,8 +159,8 @@ __global__ void __launch_bounds__(MAXT, MAXT == 256 ? (NC == 2 || NT > 0 ? 4 : F
 // One block takes rows blockIdx.x, + gridDim.x, ...; every thread keeps the same columns, so the
 // sums over the tokens stay in its registers and leave once per block, as partial sums that
 // norm_sums_kernel adds in block order (no atomics: bit-identical run to run).
-template <typename T, int NT, int NC, int MAXT>
-__global__ void __launch_bounds__(MAXT, MAXT <= 256 ? 2 : 1) norm_backward_kernel(const BackArgs a) {
+template <typename T, int NT, int NC>
+__global__ void __launch_bounds__(1024) norm_backward_kernel(const BackArgs a) {
   __shared__ float buf[2][32 * 4];
   int flip = 0;                    // the buffer of the next block-wide sums: never the one of the last
   pdl_begin();
@@ -339,7 +339,7 @@ struct Shape {
 // take one of the block sizes that are built).
 Shape shape_of(int H, bool words) {
   if (!words) {
-    const int nt = H <= 256 ? 32 : H <= 1024 ? 128 : H <= 2048 ? 256 : H <= 4096 ? 512 : 1024;
+    const int nt = H <= 1024 ? 128 : H <= 2048 ? 256 : H <= 4096 ? 512 : 1024;
     return {nt, H <= 8 * nt ? 1 : 2, 1};
   }
   const int nt = row_threads(H, 1024);
@@ -471,16 +471,11 @@ int check_post(const char* me, const PostArgs& a, int T, int H, int dtype, int f
   return MOE_OK;
 }
 
-// The kernel built for a block of this size: the fewer threads, the more registers each has. Rows of
-// 16-byte words come here only when they are too wide for the ring.
+// The kernel for rows too wide for the ring.
 template <typename T>
 auto back_kernel(const Shape& sh, bool words) {
-  if (words) return sh.nc == 2 ? norm_backward_kernel<T, 0, 2, 1024> : norm_backward_kernel<T, 0, 1, 1024>;
-  if (sh.nc == 2) return norm_backward_kernel<T, 1024, 2, 1024>;
-  return by_width<32, 128, 256, 512, 1024>(8 * sh.nt, [](auto n) {
-    constexpr int N = decltype(n)::value;
-    return norm_backward_kernel<T, N, 1, N <= 256 ? 256 : N>;
-  });
+  if (words) return sh.nc == 2 ? norm_backward_kernel<T, 0, 2> : norm_backward_kernel<T, 0, 1>;
+  return sh.nc == 2 ? norm_backward_kernel<T, 1024, 2> : norm_backward_kernel<T, 1024, 1>;
 }
 
 int launch_back(const char* me, BackArgs& a, int dtype, bool vec, void* ws, size_t ws_bytes, cudaStream_t s) {
@@ -495,15 +490,15 @@ int launch_back(const char* me, BackArgs& a, int dtype, bool vec, void* ws, size
   }
   const Shape sh = shape_of(a.H, vec);
   // the ring wants three stages (two rows ahead) and takes up to four; fewer blocks share an SM where
-  // that needs their shared memory. Two always fit: five fp32 tensors of 512 * 8 values are 80 KB.
+  // that needs their shared memory. Two always fit: five fp32 tensors of 4096 values are 80 KB.
   const int tensors = (a.dho ? 1 : 0) + (a.has_y ? 1 : 0) + (a.next ? 2 : 0) + (a.gate_mode == MOE_GATE_FULL ? 1 : 0);
-  const int stage_bytes = tensors * sh.nt * 8 * (int)dtype_size(dtype);
+  const int size = (int)dtype_size(dtype), stage_bytes = tensors * (vec ? sh.nt * 8 * size : value_region(a.H, size));
   int per_sm = ring_blocks(sh.nt, a.has_y);
   while (per_sm > 1 && kRingBytes / per_sm / stage_bytes < 3) per_sm /= 2;
   if (per_sm < 1) per_sm = 1;
   const int fit = kRingBytes / per_sm / stage_bytes;
   const int stages = fit < kRingStages ? fit : kRingStages;
-  const bool use_ring = vec && sh.nc == 1 && sh.nt <= kRingThreads && stages >= 2;
+  const bool use_ring = sh.nc == 1 && sh.nt <= kRingThreads && stages >= 2;
   // With sums over the tokens a block is worth its partial sums from two rows on, and eight blocks per
   // SM are enough (H = 2048, T = 512: 6.7 us against 8.2 with a row each; H = 1024, T = 1000: 6.7 against
   // 9.7); one or two rows take one block and no second launch (two rows of 2048: 2.9 us against 3.7).
@@ -521,7 +516,7 @@ int launch_back(const char* me, BackArgs& a, int dtype, bool vec, void* ws, size
   note_launch();
   int rc = by_type(dtype, [&](auto* p) {
     using T = std::remove_pointer_t<decltype(p)>;
-    if (use_ring) return launch_norm_ring<T>(a, blocks, sh.nt, stages, stage_bytes, s);
+    if (use_ring) return launch_norm_ring<T>(a, blocks, sh.nt, vec, stages, stage_bytes, s);
     return check_cuda(launch_pdl(back_kernel<T>(sh, vec), dim3(blocks), dim3(sh.nt), 0, s, a), "norm_backward_kernel");
   });
   if (rc || !any || blocks == 1) return rc;

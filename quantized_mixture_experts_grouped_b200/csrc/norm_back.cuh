@@ -26,8 +26,13 @@ constexpr int ring_blocks(int threads, bool has_y) {
   return (has_y ? 512 : 1024) / threads < 16 ? (has_y ? 512 : 1024) / threads : 16;
 }
 
-// Launches the ring kernel for rows of type T (one file per type, so that they compile side by side).
+// Bytes of a stage for one tensor's row moved value by value: the 16-byte granules that cover it wherever
+// it starts.
+__host__ __device__ constexpr int value_region(int H, int size) { return (H * size + 31) / 16 * 16; }
+
+// Launches the ring kernel for rows of type T (one file per type, so that they compile side by side);
+// words: rows of 16-byte words, else value by value with nt 128, 256 or kRingThreads.
 template <typename T>
-int launch_norm_ring(const BackArgs& a, int blocks, int nt, int stages, int stage_bytes, cudaStream_t s);
+int launch_norm_ring(const BackArgs& a, int blocks, int nt, bool words, int stages, int stage_bytes, cudaStream_t s);
 
 }  // namespace moe
