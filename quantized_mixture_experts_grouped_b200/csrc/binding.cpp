@@ -139,7 +139,8 @@ class Call {
     if (t.dim() == 1) {
       g.p = dense(i, what, channel, {H});
       g.mode = MOE_GATE_CHANNEL;
-    } else if (t.dim() == 2 && t.size(0) == T && t.size(1) == 1 && t.scalar_type() == at::kFloat) {
+    } else if (t.dim() == 2 && t.size(0) == T && t.size(1) == 1 && t.scalar_type() == at::kFloat &&
+               !(H == 1 && dtype == MOE_DTYPE_F32)) {         // fp32 rows of one value: per value, any stride
       g.p = dense(i, what, at::kFloat, {T, 1});
       g.mode = MOE_GATE_TOKEN;
     } else {

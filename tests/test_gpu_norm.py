@@ -367,3 +367,79 @@ def test_vectors_on_any_boundary(dt, H):
                                           wn.cpu(), dxn.cpu())
             for name, got in (("dh", dh), ("dy", dy), ("dw", dw), ("dgate", dg), ("dw_next", dn)):
                 ref.check(got, *want[name], name)
+
+
+def at(n, H, dt, off, g, ld=None, scale=1.0):
+    """Rows [n][H] that start `off` values into their buffer, ld apart (0: one row for all)."""
+    ld = H if ld is None else ld
+    buf = (torch.randn(off + max(n - 1, 0) * ld + H, generator=g) * scale).to(dt).cuda()
+    return torch.as_strided(buf, (n, H), (ld, 1), off)
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("H", [1, 3, 136, 1000, 1031, 2050, 4095])
+@pytest.mark.parametrize("T", [1, 2, 700])
+def test_rows_that_start_anywhere(dt, H, T):
+    """Every tensor at an offset of its own, contiguous and strided rows, inputs that repeat one row."""
+    g = torch.Generator().manual_seed(H + T)
+    dt = DT[dt]
+    n = 0
+
+    def new(ld=None, scale=1.0):
+        nonlocal n
+        n += 3
+        return at(T, H, dt, n % 8, g, ld, scale)
+    y, h, gate = new(scale=0.3), new(0), new(H + 3)
+    w, wn = at(1, H, dt, 5, g)[0], at(1, H, dt, 2, g)[0]
+    ho, xn = new(H + 1), new()
+    q.moe_norm_post(y, h, ho, EPS, alpha=0.5, w=w, gate=gate, w_next=wn, x_next=xn)
+    rh, bh, rx, bx = ref.norm_post(y.cpu(), h.cpu(), EPS, 0.5, True, w.cpu(), gate.cpu(), wn.cpu(), True)
+    ref.check(ho, rh, bh, "h_out")
+    ref.check(xn, rx, bx, "x_next")
+    dho, dxn, dh, dy, dg = new(0), new(), new(H + 1), new(), new(H + 5)
+    dw, dn = torch.empty(H, device="cuda"), torch.empty(H, device="cuda")
+    ws = ws_for(T, H)
+    q.moe_norm_post_backward(dho, y, dh, dy, EPS, alpha=0.5, w=w, dw=dw, gate=gate, dgate=dg, h_out=ho, w_next=wn,
+                             dx_next=dxn, dw_next=dn, ws=ws)
+    want = ref.norm_post_backward(dho.cpu(), y.cpu(), EPS, 0.5, True, w.cpu(), gate.cpu(), ho.cpu(), wn.cpu(), dxn.cpu())
+    for name, got in (("dh", dh), ("dy", dy), ("dw", dw), ("dgate", dg), ("dw_next", dn)):
+        ref.check(got, *want[name], name)
+    x, dx, dhp, res = new(), new(0), new(), new()
+    q.moe_norm_pre(y, w, EPS, x)
+    ref.check(x, *ref.norm_pre(y.cpu(), w.cpu(), EPS), "x")
+    q.moe_norm_pre_backward(dx, y, w, EPS, dhp, dres=res, dw=dw, ws=ws)
+    r, b, rw, bw = ref.norm_pre_backward(dx.cpu(), y.cpu(), w.cpu(), EPS, res.cpu())
+    ref.check(dhp, r, b, "dh pre")
+    ref.check(dw, rw, bw, "dw pre")
+    q.moe_norm_pre_backward(dx, y, w, EPS, res, dres=res)              # in place
+    assert torch.equal(res, dhp)
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("H", [3, 136, 1031])
+@pytest.mark.parametrize("T,k", [(9, 3), (900, 4)])
+def test_way_back_of_rows_that_start_anywhere(dt, H, T, k):
+    g = torch.Generator().manual_seed(H)
+    dt, E = DT[dt], 6
+    idx, wts = routing(T, E, k, g, 0.2)
+    x, xp = at(T, H, dt, 3, g), at(T * k, H, dt, 6, g, H + 1)
+    before = xp.clone()
+    i32 = dict(dtype=torch.int32, device="cuda")
+    inv, w = torch.empty((T, k), **i32), wts.cuda()
+    q.moe_dispatch(x, idx.cuda(), E, torch.empty(E, **i32), torch.empty(E + 1, **i32), torch.empty(T * k, **i32), inv, xp)
+    perm = ref.sort(idx, E)[2]
+    assert torch.equal(xp[:len(perm)], x[(perm // k).long().cuda()]) and torch.equal(xp[len(perm):], before[len(perm):])
+    out, h, ho = at(T, H, dt, 1, g), at(T, H, dt, 7, g, 0), at(T, H, dt, 4, g)
+    q.moe_combine(xp, inv, w, out)
+    r, b = ref.combine(xp.cpu(), inv.cpu(), wts)
+    ref.check(out, r, b, "out")
+    q.moe_combine_norm_post(xp, inv, w, h, ho, EPS)
+    rh, bh, _, _ = ref.norm_post(r, h.cpu(), EPS, 1.0, True, None, None, None, False, y_err=b)
+    ref.check(ho, rh, bh, "h_out")
+    if T < 100:
+        dyp, dw = at(T * k, H, dt, 5, g), torch.empty((T, k), device="cuda")
+        q.moe_combine_backward(h, xp, inv, w, dyp, dw)
+        rd, bd, rw, bw = ref.combine_backward(h.cpu(), xp.cpu(), inv.cpu(), wts)
+        live = ~rd.isnan().any(1)
+        ref.check(dyp.cpu()[live], rd[live], bd[live], "dyp")
+        ref.check(dw, rw, bw, "dwts")
