@@ -156,9 +156,10 @@ __global__ void __launch_bounds__(MAXT, MAXT == 256 ? (NC == 2 || NT > 0 ? 4 : F
   }
 }
 
-// One block takes rows blockIdx.x, + gridDim.x, ...; every thread keeps the same columns, so the
-// sums over the tokens stay in its registers and leave once per block, as partial sums that
-// norm_sums_kernel adds in block order (no atomics: bit-identical run to run).
+// The gradient for rows too wide for the ring (norm_ring.cuh; above 4096 values). One block takes rows
+// blockIdx.x, + gridDim.x, ...; every thread keeps the same columns, so the sums over the tokens stay
+// in its registers (above 8192 values spilled to local memory) and leave once per block, as partial
+// sums that norm_sums_kernel adds in block order (no atomics: bit-identical run to run).
 template <typename T, int NT, int NC>
 __global__ void __launch_bounds__(1024) norm_backward_kernel(const BackArgs a) {
   __shared__ float buf[2][32 * 4];
