@@ -284,7 +284,8 @@ int moe_route_topk_backward(const int32_t* idx, const float* wts, const float* d
 
 /* ---- Norms before and after a block, with its gate and the scaled residual. Types, strides and
  * sums as above; H <= 16384; every tensor of rows in a call has the same type `dtype`, and so have
- * the norms' weights [H] and the per-channel gate. rms(v) = v / sqrt(mean(v^2) + eps), eps > 0.
+ * the norms' weights [H] and the per-channel gate. rms(v) = v / sqrt(mean(v^2) + eps), eps > 0; a row's
+ * sum of squares has to fit fp32.
  *
  *   before the block:  x      = rms(h) * w
  *   after the block:   u      = rms(y) * w   with MOE_NORM_Y, else y

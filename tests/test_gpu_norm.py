@@ -443,3 +443,23 @@ def test_way_back_of_rows_that_start_anywhere(dt, H, T, k):
         live = ~rd.isnan().any(1)
         ref.check(dyp.cpu()[live], rd[live], bd[live], "dyp")
         ref.check(dw, rw, bw, "dwts")
+
+
+@pytest.mark.parametrize("H,pad", [(2048, 0), (1031, 0), (512, 1), (4096, 8)])
+def test_gradients_repeat(H, pad):
+    """The same bits from twenty runs, with another kernel's work before each."""
+    g = torch.Generator().manual_seed(H)
+    T, dt = 3000, torch.bfloat16
+    y, h, dho, dxn = (rows(T, H, dt, g, pad) for _ in range(4))
+    w, wn, gate = (vec(H, dt, g) for _ in range(3))
+    ws, first = ws_for(T, H), None
+    for _ in range(20):
+        dh, dy = room(T, H, dt, pad), room(T, H, dt, pad)
+        sums = [torch.full((H,), KEEP, device="cuda") for _ in range(3)]
+        ws.fill_(0xff)
+        q.moe_norm_post_backward(dho, y, dh, dy, EPS, w=w, dw=sums[0], gate=gate, dgate=sums[1], h_out=h, w_next=wn,
+                                 dx_next=dxn, dw_next=sums[2], ws=ws)
+        got = [dh, dy, *sums]
+        first = got if first is None else first
+        for a, b in zip(got, first):
+            assert torch.equal(a, b)
