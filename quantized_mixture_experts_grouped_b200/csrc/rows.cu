@@ -542,6 +542,8 @@ MOE_API int moe_dispatch(const void* x, int64_t x_stride, int dtype, const int32
   if (!counts || !offsets || (T > 0 && (!x || !idx || !perm || !inv || !xp)))
     return fail(MOE_ERR_ARG, "%s: null pointer", me);
   if (T > 0 && x == xp) return fail(MOE_ERR_ARG, "%s: xp overlaps x", me);
+  if (T > 0 && (idx == inv || idx == perm || inv == perm || idx == counts || idx == offsets))
+    return fail(MOE_ERR_ARG, "%s: idx and the index outputs overlap", me);
   if (int rc = check_stride(me, "x", x_stride, T, H, false)) return rc;
   if (int rc = check_stride(me, "xp", xp_stride, (int64_t)T * k, H, true)) return rc;
   return launch_dispatch(x, x_stride, dtype_size(dtype), idx, T, H, E, k, counts, offsets, perm, inv, xp, xp_stride,

@@ -44,6 +44,16 @@ def test_dispatch_refusals(kw, code):
     assert b"moe_dispatch" in q.lib.moe_last_error_string()
 
 
+def test_dispatch_refuses_shared_index_buffers():
+    """Each block reads every id while others write places: none may share a buffer."""
+    ids = [ctypes.c_void_p(1 << i) for i in range(20, 26)]
+    apart = dict(zip(("idx", "counts", "offsets", "perm", "inv", "xp"), ids))
+    for name in ("counts", "offsets", "perm", "inv"):
+        assert dispatch(**{**apart, name: apart["idx"]}) == ARG
+        assert b"overlap" in q.lib.moe_last_error_string(), name
+    assert dispatch(**{**apart, "perm": apart["inv"]}) == ARG
+
+
 def test_combine_refusals():
     f = lambda yp=P, ldy=8, ydt=F32, inv=P, w=P, T=4, H=8, k=2, out=P2, ldo=8, odt=BF16: q.lib.moe_combine(
         yp, ldy, ydt, inv, w, T, H, k, out, ldo, odt, None)
