@@ -502,9 +502,12 @@ int launch_back(const char* me, BackArgs& a, int dtype, bool vec, void* ws, size
   const bool use_ring = sh.nc == 1 && sh.nt <= kRingThreads && stages >= 2;
   // With sums over the tokens a block is worth its partial sums from two rows on, and eight blocks per
   // SM are enough (H = 2048, T = 512: 6.7 us against 8.2 with a row each; H = 1024, T = 1000: 6.7 against
-  // 9.7); one or two rows take one block and no second launch (two rows of 2048: 2.9 us against 3.7).
+  // 9.7); one or two rows, or up to four narrow ones of words, take one block and no second launch (two rows of
+  // 2048: 2.9 us against 3.7; four of 512: 3.3 against 3.4, and 3.7 against 5.1 where the host's time for
+  // the launches counts).
   int blocks = back_blocks(a.T, a.H, any && per_sm > 8 ? 8 : per_sm);
-  if (any) blocks = a.T <= 2 ? 1 : std::min(blocks, std::max(norm_sms(), ceil_div(a.T, 2)));
+  const bool one = a.T <= 2 || (vec && a.T <= 4 && a.T * a.H <= 6144);
+  if (any) blocks = one ? 1 : std::min(blocks, std::max(norm_sms(), ceil_div(a.T, 2)));
   a.part_ld = part_stride(a.H);
   if (any && blocks > 1) {
     const size_t need = norm_ws(a.T, a.H);
