@@ -416,7 +416,8 @@ PyObject* norm_post_backward(PyObject* const* args, Py_ssize_t n) {
   const int flags = (norm_y ? MOE_NORM_Y : 0) | (next ? MOE_NORM_NEXT : 0);
   return c.run(16, [&](moe_stream_t s) {
     return moe_norm_post_backward(d.p, d.ld, y.p, y.ld, d.dtype, w, g.p, g.ld, g.mode, alpha, eps, (int)T, (int)H,
-                                  flags, ho.p, ho.ld, wn, dx.p, dx.ld, dh.p, dh.ld, dy.p, dy.ld, dw, const_cast<void*>(dg.p),
+                                  flags, ho.p, ho.ld, wn, dx.p, dx.ld, dh.p, dh.ld, dy.p, dy.ld, dw,
+                                  const_cast<void*>(dg.p),
                                   dg.ld, dwn, ws, bytes, s);
   });
 }

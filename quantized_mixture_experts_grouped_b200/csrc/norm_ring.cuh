@@ -372,7 +372,8 @@ int by_gate(const BackArgs& a, int blocks, int nt, int stages, int stage_bytes, 
 
 template <typename T, int MAXT, int NT>
 int by_flags(const BackArgs& a, int blocks, int nt, int stages, int stage_bytes, cudaStream_t s) {
-  if (!a.has_y) return launch_one<T, MAXT, NT, false, false, true, MOE_GATE_NONE>(a, blocks, nt, stages, stage_bytes, s);
+  if (!a.has_y)
+    return launch_one<T, MAXT, NT, false, false, true, MOE_GATE_NONE>(a, blocks, nt, stages, stage_bytes, s);
   if (a.norm_y)
     return a.next ? by_gate<T, MAXT, NT, true, true>(a, blocks, nt, stages, stage_bytes, s)
                   : by_gate<T, MAXT, NT, true, false>(a, blocks, nt, stages, stage_bytes, s);

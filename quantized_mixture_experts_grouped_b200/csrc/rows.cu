@@ -485,7 +485,8 @@ int launch_combine_rows(const void* yp, int64_t ldy, int ydt, const int32_t* inv
   return by_types(ydt, odt, [&](auto* y, auto* o) {
     using YT = std::remove_pointer_t<decltype(y)>;
     using OT = std::remove_pointer_t<decltype(o)>;
-    auto kern = !vec    ? by_width<32, 128, 256>(H, [](auto n) { return combine_rows_kernel<YT, OT, decltype(n)::value, 4, 1>; })
+    auto values = [](auto n) { return combine_rows_kernel<YT, OT, decltype(n)::value, 4, 1>; };
+    auto kern = !vec    ? by_width<32, 128, 256>(H, values)
                 : eight ? combine_rows_kernel<YT, OT, 0, 8, 1>
                 : !two  ? combine_rows_kernel<YT, OT, 0, 4, 1>
                 : k <= 2 ? combine_rows_kernel<YT, OT, 0, 2, 2>
@@ -602,8 +603,8 @@ MOE_API int moe_combine_backward(const void* dout, int64_t dout_stride, int dout
   return by_types(yp_dtype, dout_dtype, [&](auto* y, auto* o) {
     using YT = std::remove_pointer_t<decltype(y)>;
     using OT = std::remove_pointer_t<decltype(o)>;
-    auto kern = vec ? combine_backward_kernel<YT, OT, 0>
-                    : by_width<32, 128, 256>(H, [](auto n) { return combine_backward_kernel<YT, OT, decltype(n)::value>; });
+    auto values = [](auto n) { return combine_backward_kernel<YT, OT, decltype(n)::value>; };
+    auto kern = vec ? combine_backward_kernel<YT, OT, 0> : by_width<32, 128, 256>(H, values);
     return check_cuda(launch_pdl(kern, dim3(T), dim3(vec ? row_threads(H, kRowThreads) : value_threads(H)), 0,
                                  reinterpret_cast<cudaStream_t>(stream), static_cast<const OT*>(dout), dout_stride,
                                  static_cast<const YT*>(yp), yp_stride, inv, wts, k, T * k, H, static_cast<YT*>(dyp),

@@ -401,7 +401,8 @@ def test_rows_that_start_anywhere(dt, H, T):
     ws = ws_for(T, H)
     q.moe_norm_post_backward(dho, y, dh, dy, EPS, alpha=0.5, w=w, dw=dw, gate=gate, dgate=dg, h_out=ho, w_next=wn,
                              dx_next=dxn, dw_next=dn, ws=ws)
-    want = ref.norm_post_backward(dho.cpu(), y.cpu(), EPS, 0.5, True, w.cpu(), gate.cpu(), ho.cpu(), wn.cpu(), dxn.cpu())
+    want = ref.norm_post_backward(dho.cpu(), y.cpu(), EPS, 0.5, True, w.cpu(), gate.cpu(), ho.cpu(), wn.cpu(),
+                                  dxn.cpu())
     for name, got in (("dh", dh), ("dy", dy), ("dw", dw), ("dgate", dg), ("dw_next", dn)):
         ref.check(got, *want[name], name)
     x, dx, dhp, res = new(), new(0), new(), new()
@@ -426,7 +427,8 @@ def test_way_back_of_rows_that_start_anywhere(dt, H, T, k):
     before = xp.clone()
     i32 = dict(dtype=torch.int32, device="cuda")
     inv, w = torch.empty((T, k), **i32), wts.cuda()
-    q.moe_dispatch(x, idx.cuda(), E, torch.empty(E, **i32), torch.empty(E + 1, **i32), torch.empty(T * k, **i32), inv, xp)
+    q.moe_dispatch(x, idx.cuda(), E, torch.empty(E, **i32), torch.empty(E + 1, **i32), torch.empty(T * k, **i32), inv,
+                   xp)
     perm = ref.sort(idx, E)[2]
     assert torch.equal(xp[:len(perm)], x[(perm // k).long().cuda()]) and torch.equal(xp[len(perm):], before[len(perm):])
     out, h, ho = at(T, H, dt, 1, g), at(T, H, dt, 7, g, 0), at(T, H, dt, 4, g)
