@@ -509,7 +509,7 @@ int launch_back(const char* me, BackArgs& a, int dtype, bool vec, void* ws, size
   const bool one = a.T <= 2 || (vec && a.T <= 4 && a.T * a.H <= 6144);
   if (any) blocks = one ? 1 : std::min(blocks, std::max(norm_sms(), ceil_div(a.T, 2)));
   a.part_ld = part_stride(a.H);
-  if (any && blocks > 1) {
+  if (any) {                       // asked for whether or not this call's size uses it
     const size_t need = norm_ws(a.T, a.H);
     if (!ws || ws_bytes < need)
       return fail(MOE_ERR_ARG, "%s: workspace of %zu bytes is smaller than the %zu needed", me, ws ? ws_bytes : 0,
