@@ -350,13 +350,14 @@ Shape shape_of(int H, bool words) {
 // Forward, up to 4096 values: 256 threads, with two chunks per thread (half as many exchanges per row,
 // twice the loads in flight per thread: T = 2048, H = 2048, bf16, post with next norm 6.2 us against
 // 7.1), but one up to 256 rows of 2048 values, where a row's own latency counts (2.2 against 2.4 at
-// T = 1). Wider rows take more threads. Single values: two chunks from 1025 on.
+// T = 1); up to 256 wider rows take one chunk in more threads too, as any do from 4097 on. Single values:
+// two chunks from 1025 on.
 Shape shape_forward(int rows, int H, bool words) {
   if (!words) {
     const int nc = H <= 1024 ? 1 : 2, nt = H <= 256 ? 32 : H <= 2048 ? 128 : H <= 4096 ? 256 : 1024;
     return {nt, nc, nt > 256 ? 1 : 256 / nt};
   }
-  if (H > 4096) return shape_of(H, true);
+  if (H > 4096 || (H > 2048 && rows <= 256)) return shape_of(H, true);
   const int nc = H <= 256 || (H <= 2048 && rows <= 256) ? 1 : 2, nt = row_threads(ceil_div(H, nc), 256);
   return {nt, nc, 256 / nt < kBlockRows ? 256 / nt : kBlockRows};
 }

@@ -290,7 +290,7 @@ int dispatch_units(const void* x, int64_t ldx, const int32_t* idx, int T, int E,
 // ------------------------------------------------------------------------------------- combine
 
 template <typename YT, typename OT, int NT, int B, int NC>
-__global__ void __launch_bounds__(kRowThreads, NC == 2 || sizeof(YT) == 2 || NT > 0 ? 4 : 1)
+__global__ void __launch_bounds__(kRowThreads, NC == 2 || (NT == 0 && sizeof(YT) == 2) || (NT > 0 && B == 4) ? 4 : 1)
     combine_rows_kernel(const YT* __restrict__ yp, int64_t ldy, const int32_t* __restrict__ inv,
                         const float* __restrict__ wts, int T, int k, int P, int H, OT* __restrict__ out, int64_t ldo) {
   pdl_begin();
@@ -307,8 +307,9 @@ __global__ void __launch_bounds__(kRowThreads, NC == 2 || sizeof(YT) == 2 || NT 
 // pass by: each is read once (its dot product with dout) and its gradient row written once. The
 // dot products of up to kDots choices are reduced together at the end of the row.
 constexpr int kDots = 8;
+constexpr int kFewPairs = 512;
 
-template <typename YT, typename OT, int NT>
+template <typename YT, typename OT>
 __global__ void __launch_bounds__(kRowThreads, 4)
     combine_backward_kernel(const OT* __restrict__ dout, int64_t ldo, const YT* __restrict__ yp, int64_t ldy,
                             const int32_t* __restrict__ inv, const float* __restrict__ wts, int k, int P, int H,
@@ -316,7 +317,7 @@ __global__ void __launch_bounds__(kRowThreads, 4)
   __shared__ float buf[2][32 * kDots];
   pdl_begin();
   const int64_t t = blockIdx.x;
-  const int nt = NT ? NT : blockDim.x, tid = threadIdx.x;
+  const int nt = blockDim.x, tid = threadIdx.x;
   const int chunks = (H + 8 * nt - 1) / (8 * nt);
   const int32_t* it = inv + t * k;
   const float* wt = wts + t * k;
@@ -338,7 +339,7 @@ __global__ void __launch_bounds__(kRowThreads, 4)
     for (int b = 0; b < kDots; ++b) part[b] = f2(0.f, 0.f);
     for (int c = 0; c < chunks; ++c) {
       F2 d[4];
-      load8<NT>(dout + t * ldo, c, nt, tid, H, d);
+      load8<0>(dout + t * ldo, c, nt, tid, H, d);
       // four choices' words at a time and four blocks per SM: T = 2048, k = 8, H = 2048 took 54 us for
       // the whole gradient with eight and three, 49 with four and five (spills), 44 like this
       constexpr int B = 4;
@@ -350,7 +351,7 @@ __global__ void __launch_bounds__(kRowThreads, 4)
 #pragma unroll
           for (int b = 0; b < B; ++b) {
             const bool on = pos[b0 + b] >= 0;
-            r[b] = load_raw<NT>(yp + (int64_t)(on ? pos[b0 + b] : 0) * ldy, c, nt, tid, on ? H : 0);
+            r[b] = load_raw<0>(yp + (int64_t)(on ? pos[b0 + b] : 0) * ldy, c, nt, tid, on ? H : 0);
           }
         }
         if (dyp) {          // does not wait for yp's rows
@@ -362,7 +363,7 @@ __global__ void __launch_bounds__(kRowThreads, 4)
 #pragma unroll
             for (int e = 0; e < 4; ++e) g[e] = mul2(w2, d[e]);
             const bool on = pos[b0 + b] >= 0;
-            store8<NT>(dyp + (int64_t)(on ? pos[b0 + b] : 0) * lddy, c, nt, tid, on ? H : 0, g);
+            store8<0>(dyp + (int64_t)(on ? pos[b0 + b] : 0) * lddy, c, nt, tid, on ? H : 0, g);
           }
         }
         if (dwts) {
@@ -370,7 +371,7 @@ __global__ void __launch_bounds__(kRowThreads, 4)
           for (int b = 0; b < B; ++b) {
             if (j0 + b0 + b >= k) break;
             F2 v[4];
-            raw_pairs<NT>(r[b], v);
+            raw_pairs<0>(r[b], v);
 #pragma unroll
             for (int e = 0; e < 4; ++e) part[b0 + b] = fma2(d[e], v[e], part[b0 + b]);
           }
@@ -387,6 +388,50 @@ __global__ void __launch_bounds__(kRowThreads, 4)
         if (tid == b && j0 + b < k) dwts[t * k + j0 + b] = pos[b] >= 0 ? dot[b] : 0.f;
     }
   }
+}
+
+// The same with one block per pair: no choice waits for another, and dout's row, read k times, comes from
+// L2. For few pairs (T = 1, k = 8, H = 2048, bf16: 1.7 us against 2.8 with a block per token; T = 64: 2.5
+// against 3.1; T = 256: 5.0 against 4.0), for rows moved value by value (T = 2048, k = 2, H = 1031: 9.5
+// against 20; k = 8: 33 against 45) and for wide rows of one or two choices (T = 8192, k = 2, H = 2048: 40
+// against 50; k = 4: 16 against 13 at T = 2048).
+template <typename YT, typename OT, int NT>
+__global__ void __launch_bounds__(kRowThreads)
+    combine_pair_backward_kernel(const OT* __restrict__ dout, int64_t ldo, const YT* __restrict__ yp, int64_t ldy,
+                                 const int32_t* __restrict__ inv, const float* __restrict__ wts, int k, int P, int H,
+                                 YT* __restrict__ dyp, int64_t lddy, float* __restrict__ dwts) {
+  __shared__ float buf[32];
+  pdl_begin();
+  const int pair = blockIdx.x, nt = NT ? NT : blockDim.x, tid = threadIdx.x;
+  const int pos = inv[pair];
+  const float w = wts[pair];
+  if ((unsigned)pos >= (unsigned)P) {
+    if (dwts && tid == 0) dwts[pair] = 0.f;
+    return;
+  }
+  const OT* drow = dout + (int64_t)(pair / k) * ldo;
+  const int chunks = (H + 8 * nt - 1) / (8 * nt);
+  const F2 w2 = f2(w, w);
+  F2 part = f2(0.f, 0.f);
+#pragma unroll 2
+  for (int c = 0; c < chunks; ++c) {
+    F2 d[4], v[4];
+    load8<NT>(drow, c, nt, tid, H, d);
+    if (dwts) {
+      load8<NT>(yp + (int64_t)pos * ldy, c, nt, tid, H, v);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) part = fma2(d[e], v[e], part);
+    }
+    if (dyp) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) d[e] = mul2(w2, d[e]);
+      store8<NT>(dyp + (int64_t)pos * lddy, c, nt, tid, H, d);
+    }
+  }
+  if (!dwts) return;
+  float dot[1] = {sum_of(part)};
+  block_sums<1>(dot, buf);
+  if (tid == 0) dwts[pair] = dot[0];
 }
 
 // ------------------------------------------------------------------------------------- router
@@ -476,7 +521,7 @@ int launch_combine_rows(const void* yp, int64_t ldy, int ydt, const int32_t* inv
   // chunk of eight for more choices in 16 bits (T = 2048, k = 8, H = 2048 with sort and copy: 34.4 us
   // against 35.5 with two chunks of four and 37.3 of two), and in fp32 for so few tokens that a token's
   // own latency counts (T = 2048: 18 us against 16 with two chunks of two; T = 1: 1.7 against 4.2).
-  // Single values: one chunk of four. Narrow rows share a block.
+  // Single values: one chunk of four, of eight for few tokens. Narrow rows share a block.
   const bool wide = ydt == MOE_DTYPE_F32;
   const bool eight = vec && k > 4 && (!wide || T <= 256), two = vec && !eight && H > 256;
   const int nt = vec ? row_threads(ceil_div(H, two ? 2 : 1), kRowThreads) : value_threads(H), ny = kRowThreads / nt;
@@ -486,7 +531,8 @@ int launch_combine_rows(const void* yp, int64_t ldy, int ydt, const int32_t* inv
     using YT = std::remove_pointer_t<decltype(y)>;
     using OT = std::remove_pointer_t<decltype(o)>;
     auto values = [](auto n) { return combine_rows_kernel<YT, OT, decltype(n)::value, 4, 1>; };
-    auto kern = !vec    ? by_width<32, 128, 256>(H, values)
+    auto few = [](auto n) { return combine_rows_kernel<YT, OT, decltype(n)::value, 8, 1>; };
+    auto kern = !vec    ? (k > 4 && T <= 256 ? by_width<32, 128, 256>(H, few) : by_width<32, 128, 256>(H, values))
                 : eight ? combine_rows_kernel<YT, OT, 0, 8, 1>
                 : !two  ? combine_rows_kernel<YT, OT, 0, 4, 1>
                 : k <= 2 ? combine_rows_kernel<YT, OT, 0, 2, 2>
@@ -603,9 +649,11 @@ MOE_API int moe_combine_backward(const void* dout, int64_t dout_stride, int dout
   return by_types(yp_dtype, dout_dtype, [&](auto* y, auto* o) {
     using YT = std::remove_pointer_t<decltype(y)>;
     using OT = std::remove_pointer_t<decltype(o)>;
-    auto values = [](auto n) { return combine_backward_kernel<YT, OT, decltype(n)::value>; };
-    auto kern = vec ? combine_backward_kernel<YT, OT, 0> : by_width<32, 128, 256>(H, values);
-    return check_cuda(launch_pdl(kern, dim3(T), dim3(vec ? row_threads(H, kRowThreads) : value_threads(H)), 0,
+    auto pairs = [](auto n) { return combine_pair_backward_kernel<YT, OT, decltype(n)::value>; };
+    const bool few = T * k <= kFewPairs || !vec || (k <= 2 && H > 1024);
+    auto kern = !few ? combine_backward_kernel<YT, OT>
+                : vec ? combine_pair_backward_kernel<YT, OT, 0> : by_width<32, 128, 256>(H, pairs);
+    return check_cuda(launch_pdl(kern, dim3(few ? T * k : T), dim3(vec ? row_threads(H, kRowThreads) : value_threads(H)), 0,
                                  reinterpret_cast<cudaStream_t>(stream), static_cast<const OT*>(dout), dout_stride,
                                  static_cast<const YT*>(yp), yp_stride, inv, wts, k, T * k, H, static_cast<YT*>(dyp),
                                  dyp_stride, dwts),
