@@ -307,7 +307,7 @@ __global__ void __launch_bounds__(kRowThreads, NC == 2 || (NT == 0 && sizeof(YT)
 // pass by: each is read once (its dot product with dout) and its gradient row written once. The
 // dot products of up to kDots choices are reduced together at the end of the row.
 constexpr int kDots = 8;
-constexpr int kFewPairs = 512;
+constexpr int kFewPairs = 1024;
 
 template <typename YT, typename OT>
 __global__ void __launch_bounds__(kRowThreads, 4)
@@ -390,48 +390,78 @@ __global__ void __launch_bounds__(kRowThreads, 4)
   }
 }
 
-// The same with one block per pair: no choice waits for another, and dout's row, read k times, comes from
-// L2. For few pairs (T = 1, k = 8, H = 2048, bf16: 1.7 us against 2.8 with a block per token; T = 64: 2.5
-// against 3.1; T = 256: 5.0 against 4.0), for rows moved value by value (T = 2048, k = 2, H = 1031: 9.5
-// against 20; k = 8: 33 against 45) and for wide rows of one or two choices (T = 8192, k = 2, H = 2048: 40
-// against 50; k = 4: 16 against 13 at T = 2048).
-template <typename YT, typename OT, int NT>
+// The same with a block per token and group of G choices: groups do not wait for one another, and dout's
+// row, read once per group, comes from L2 after the first. One choice in a group where latency counts
+// (T = 1, k = 8, H = 2048, bf16: 1.7 us against 2.8 with a block per token; 512 pairs: 2.3 against 3.1;
+// 1024: 3.3 against 3.2, fp32 4.3 against 5.0; 2048: 4.8 against 4.0) or where one or two wide rows stream (T = 8192, k = 2, H = 2048: 36 against 38
+// with two and 50 with a block per token). Rows moved value by value are bound by their single loads and
+// stores, of which a group shares dout's (T = 2048, k = 8, H = 2048, bf16: 48, 42, 36, 42 us with 1, 2, 4,
+// 8; H = 1031: 32, 26, 22; T = 4096, H = 255: 34, 17, 9.1, 8.4). Words of fp32 take two (T = 2048, k = 8,
+// H = 2048: 51, 45, 46, 51 against 54 with a block per token; k = 4: 27, 24, 25, 29 against 30; T = 4096,
+// k = 8, H = 512: 35, 23, 23, 25 against 29, but H = 128: 34, 17, 8.9, 6.1 against 8.1), 16-bit words a
+// block per token (T = 2048, k = 8: 35, 37, 32, 43 against 27) unless there are two narrow ones (T = 8192,
+// H = 512: 17, 8.9 against 10).
+template <typename YT, typename OT, int NT, int G>
 __global__ void __launch_bounds__(kRowThreads)
-    combine_pair_backward_kernel(const OT* __restrict__ dout, int64_t ldo, const YT* __restrict__ yp, int64_t ldy,
+    combine_group_backward_kernel(const OT* __restrict__ dout, int64_t ldo, const YT* __restrict__ yp, int64_t ldy,
                                  const int32_t* __restrict__ inv, const float* __restrict__ wts, int k, int P, int H,
                                  YT* __restrict__ dyp, int64_t lddy, float* __restrict__ dwts) {
-  __shared__ float buf[32];
+  __shared__ float buf[32 * G];
   pdl_begin();
-  const int pair = blockIdx.x, nt = NT ? NT : blockDim.x, tid = threadIdx.x;
-  const int pos = inv[pair];
-  const float w = wts[pair];
-  if ((unsigned)pos >= (unsigned)P) {
-    if (dwts && tid == 0) dwts[pair] = 0.f;
+  const int groups = (k + G - 1) / G;
+  const int nt = NT ? NT : blockDim.x, tid = threadIdx.x;
+  const int t = blockIdx.x / groups, j0 = (blockIdx.x - t * groups) * G;
+  const int64_t first = (int64_t)t * k + j0;
+  int pos[G];
+  float w[G];
+  bool any = false;
+#pragma unroll
+  for (int g = 0; g < G; ++g) {
+    const bool in = j0 + g < k;
+    pos[g] = in ? inv[first + g] : -1;
+    w[g] = in ? wts[first + g] : 0.f;
+    if ((unsigned)pos[g] >= (unsigned)P) pos[g] = -1;
+    any |= pos[g] >= 0;
+  }
+  if (!any) {
+    if (dwts && tid < G && j0 + tid < k) dwts[first + tid] = 0.f;
     return;
   }
-  const OT* drow = dout + (int64_t)(pair / k) * ldo;
+  const OT* drow = dout + (int64_t)t * ldo;
   const int chunks = (H + 8 * nt - 1) / (8 * nt);
-  const F2 w2 = f2(w, w);
-  F2 part = f2(0.f, 0.f);
+  F2 part[G];
+#pragma unroll
+  for (int g = 0; g < G; ++g) part[g] = f2(0.f, 0.f);
 #pragma unroll 2
   for (int c = 0; c < chunks; ++c) {
-    F2 d[4], v[4];
+    F2 d[4];
     load8<NT>(drow, c, nt, tid, H, d);
-    if (dwts) {
-      load8<NT>(yp + (int64_t)pos * ldy, c, nt, tid, H, v);
 #pragma unroll
-      for (int e = 0; e < 4; ++e) part = fma2(d[e], v[e], part);
-    }
-    if (dyp) {
+    for (int g = 0; g < G; ++g) {
+      if (pos[g] < 0) continue;
+      if (dwts) {
+        F2 v[4];
+        load8<NT>(yp + (int64_t)pos[g] * ldy, c, nt, tid, H, v);
 #pragma unroll
-      for (int e = 0; e < 4; ++e) d[e] = mul2(w2, d[e]);
-      store8<NT>(dyp + (int64_t)pos * lddy, c, nt, tid, H, d);
+        for (int e = 0; e < 4; ++e) part[g] = fma2(d[e], v[e], part[g]);
+      }
+      if (dyp) {
+        F2 o[4];
+        const F2 w2 = f2(w[g], w[g]);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[e] = mul2(w2, d[e]);
+        store8<NT>(dyp + (int64_t)pos[g] * lddy, c, nt, tid, H, o);
+      }
     }
   }
   if (!dwts) return;
-  float dot[1] = {sum_of(part)};
-  block_sums<1>(dot, buf);
-  if (tid == 0) dwts[pair] = dot[0];
+  float dot[G];
+#pragma unroll
+  for (int g = 0; g < G; ++g) dot[g] = sum_of(part[g]);
+  block_sums<G>(dot, buf);
+#pragma unroll
+  for (int g = 0; g < G; ++g)
+    if (tid == g && j0 + g < k) dwts[first + g] = pos[g] >= 0 ? dot[g] : 0.f;
 }
 
 // ------------------------------------------------------------------------------------- router
@@ -649,12 +679,20 @@ MOE_API int moe_combine_backward(const void* dout, int64_t dout_stride, int dout
   return by_types(yp_dtype, dout_dtype, [&](auto* y, auto* o) {
     using YT = std::remove_pointer_t<decltype(y)>;
     using OT = std::remove_pointer_t<decltype(o)>;
-    auto pairs = [](auto n) { return combine_pair_backward_kernel<YT, OT, decltype(n)::value>; };
-    const bool few = T * k <= kFewPairs || !vec || (k <= 2 && H > 1024);
-    auto kern = !few ? combine_backward_kernel<YT, OT>
-                : vec ? combine_pair_backward_kernel<YT, OT, 0> : by_width<32, 128, 256>(H, pairs);
-    return check_cuda(launch_pdl(kern, dim3(few ? T * k : T), dim3(vec ? row_threads(H, kRowThreads) : value_threads(H)), 0,
-                                 reinterpret_cast<cudaStream_t>(stream), static_cast<const OT*>(dout), dout_stride,
+    // choices in a group (0: a block per token); measured at combine_group_backward_kernel
+    const int G = T * k <= kFewPairs || k == 1 || (vec && k == 2 && H > 1024) ? 1
+                  : !vec                                                   ? (k == 2 ? 2 : 4)
+                  : k == 2 || (sizeof(YT) == 4 && H >= 512)                ? 2 : 0;
+    auto form = [&](auto g) {
+      auto by_nt = [](auto n) { return combine_group_backward_kernel<YT, OT, decltype(n)::value, decltype(g)::value>; };
+      return vec ? by_nt(std::integral_constant<int, 0>()) : by_width<32, 128, 256>(H, by_nt);
+    };
+    auto kern = G == 0   ? combine_backward_kernel<YT, OT>
+                : G == 1 ? form(std::integral_constant<int, 1>())
+                : G == 2 ? form(std::integral_constant<int, 2>())
+                         : form(std::integral_constant<int, 4>());
+    const dim3 grid(G ? T * ceil_div(k, G) : T), block(vec ? row_threads(H, kRowThreads) : value_threads(H));
+    return check_cuda(launch_pdl(kern, grid, block, 0, reinterpret_cast<cudaStream_t>(stream), static_cast<const OT*>(dout), dout_stride,
                                  static_cast<const YT*>(yp), yp_stride, inv, wts, k, T * k, H, static_cast<YT*>(dyp),
                                  dyp_stride, dwts),
                       "combine_backward_kernel");

@@ -190,6 +190,15 @@ def test_combine_and_gradients(T, E, k, H, ydt, odt, drop, pad):
         ref.check(dx, *ref.combine(yp.cpu(), inv, None), "dx")
 
 
+@pytest.mark.parametrize("T,E,k,H,pad", [(300, 16, 5, 1031, 0), (300, 16, 8, 1024, 1), (700, 8, 2, 255, 0), (1100, 8, 1, 333, 3),
+                                         (260, 16, 7, 512, 0), (600, 8, 2, 640, 8), (600, 8, 2, 1032, 0), (400, 8, 3, 504, 0),
+                                         (1100, 4, 1, 64, 0), (140, 40, 33, 600, 0), (130, 9, 9, 65, 0)])
+@pytest.mark.parametrize("ydt,odt", TYPES)
+def test_gradients_of_many_pairs(T, E, k, H, pad, ydt, odt):
+    """Groups of one, two and four choices, the last not full, words and single values, tokens with none."""
+    test_combine_and_gradients(T, E, k, H, ydt, odt, 0.4, pad)
+
+
 def test_combine_ignores_what_dropped_rows_hold():
     """Infinities and NaN in rows no pair points to, and weights of dropped choices, change nothing."""
     g = torch.Generator().manual_seed(9)
