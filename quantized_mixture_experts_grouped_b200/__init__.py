@@ -269,7 +269,8 @@ def moe_norm_pre_backward(dx, h, w, eps: float, dh, dres=None, dw=None, ws=None,
 def moe_norm_post(y, h, h_out, eps: float, alpha: float = 1.0, norm_y: bool = True, w=None, gate=None, w_next=None,
                   x_next=None, stream=None):
     """h_out = alpha * h + gate * u with u = rms(y) * w (norm_y) or y, and with x_next given
-    x_next = rms(h_out) * w_next. gate: None, [H], fp32 [T][1] or [T][H]. h_out may be h."""
+    x_next = rms(h_out) * w_next. gate: None, [H], fp32 [T][1] or [T] (one value per token), or [T][H].
+    fp32 rows with T = H take a single dimension as [H]. h_out may be h."""
     _rows.norm_post(y, h, h_out, eps, alpha, norm_y, w, gate, w_next, x_next, stream)
 
 
@@ -282,8 +283,8 @@ def moe_combine_norm_post(yp, inv, wts, h, h_out, eps: float, alpha: float = 1.0
 def moe_norm_post_backward(dh_out, y, dh, dy, eps: float, alpha: float = 1.0, norm_y: bool = True, w=None, dw=None,
                            gate=None, dgate=None, h_out=None, w_next=None, dx_next=None, dw_next=None, ws=None,
                            stream=None):
-    """Gradients of moe_norm_post: dh, dy, and where given dw, dw_next (fp32 [H]) and dgate (fp32 [H],
-    fp32 [T][1] or rows). With dx_next given, h_out is the forward's output. Gradients of vectors need
+    """Gradients of moe_norm_post: dh, dy, and where given dw, dw_next (fp32 [H]) and dgate (fp32 [H], fp32
+    [T][1] or [T], or rows, as the gate is). With dx_next given, h_out is the forward's output. Gradients of vectors need
     ws, a workspace of moe_norm_workspace_bytes. dh may be dh_out."""
     _rows.norm_post_backward(dh_out, y, dh, dy, eps, alpha, norm_y, w, dw, gate, dgate, h_out, w_next, dx_next,
                              dw_next, ws, stream)

@@ -130,15 +130,22 @@ class Call {
     return static_cast<int32_t*>(p);
   }
 
-  // What broadcasts over the rows: [H] per channel (`channel`: its type), fp32 [T][1] per token,
-  // [T][H] of type dtype per value.
-  Gate gate(int i, const char* what, int64_t T, int64_t H, int dtype, at::ScalarType channel) {
+  // What broadcasts over the rows: [H] per channel (`channel`: its type), fp32 [T][1] or [T] per token,
+  // [T][H] of type dtype per value. A single dimension that fits both ways (fp32 channels, T = H) is per
+  // channel, unless the call's gate, of mode `as`, says otherwise.
+  Gate gate(int i, const char* what, int64_t T, int64_t H, int dtype, at::ScalarType channel, int as = -1) {
     Gate g;
     if (none(i)) return g;
     const at::Tensor& t = tensor(i, what);
     if (t.dim() == 1) {
-      g.p = dense(i, what, channel, {H});
-      g.mode = MOE_GATE_CHANNEL;
+      const bool fits = t.scalar_type() == channel && t.size(0) == H;
+      if (as == MOE_GATE_TOKEN || (as < 0 && !fits && t.scalar_type() == at::kFloat && t.size(0) == T)) {
+        g.p = dense(i, what, at::kFloat, {T});
+        g.mode = MOE_GATE_TOKEN;
+      } else {
+        g.p = dense(i, what, channel, {H});
+        g.mode = MOE_GATE_CHANNEL;
+      }
     } else if (t.dim() == 2 && t.size(0) == T && t.size(1) == 1 && t.scalar_type() == at::kFloat &&
                !(H == 1 && dtype == MOE_DTYPE_F32)) {         // fp32 rows of one value: per value, any stride
       g.p = dense(i, what, at::kFloat, {T, 1});
@@ -405,7 +412,7 @@ PyObject* norm_post_backward(PyObject* const* args, Py_ssize_t n) {
   const void* w = c.maybe_dense(7, "w", type, {H});
   float* dw = static_cast<float*>(c.maybe_dense(8, "dw", at::kFloat, {H}));
   const Gate g = c.gate(9, "gate", T, H, d.dtype, type);
-  const Gate dg = c.gate(10, "dgate", T, H, d.dtype, at::kFloat);
+  const Gate dg = c.gate(10, "dgate", T, H, d.dtype, at::kFloat, g.mode);
   if (dg.p && dg.mode != g.mode) c.refuse("dgate has another form than gate");
   const Rows ho = c.maybe_rows(11, "h_out", T, H, d.dtype);
   const void* wn = c.maybe_dense(12, "w_next", type, {H});
