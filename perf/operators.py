@@ -168,7 +168,7 @@ def prepare(case, seed):
         s["w"] = rows(1, 0.1, mean=1.0)[0] if c["norm_y"] else None
         s["w_next"] = rows(1, 0.1, mean=1.0)[0] if c["next"] else None
         s["gate"] = {"none": lambda: None, "channel": lambda: rows(1, 0.2, mean=0.5)[0],
-                     "token": lambda: torch.rand((T, 1), generator=g, device=dev),
+                     "token": lambda: torch.rand(T, generator=g, device=dev),
                      "full": lambda: rows(T, 0.2, mean=0.5)}[c["gate"]]()
         if op != "post_bwd":
             s["h_out"] = room(T)
@@ -182,7 +182,7 @@ def prepare(case, seed):
             s["dw"] = torch.zeros(H, device=dev) if c["norm_y"] else None
             s["dw_next"] = torch.zeros(H, device=dev) if c["next"] else None
             s["dgate"] = {"none": lambda: None, "channel": lambda: torch.zeros(H, device=dev),
-                          "token": lambda: torch.zeros((T, 1), device=dev), "full": lambda: room(T)}[c["gate"]]()
+                          "token": lambda: torch.zeros(T, device=dev), "full": lambda: room(T)}[c["gate"]]()
     return s
 
 
@@ -303,7 +303,10 @@ def _plain_pre(s):
 
 
 def _gate(s):
-    return 1.0 if s["gate"] is None else s["gate"].float()      # [H], [T][1] or [T][H]
+    g = s["gate"]
+    if g is None:
+        return 1.0
+    return g.float()[:, None] if s["case"]["gate"] == "token" else g.float()
 
 
 def _after(s, y):
@@ -336,7 +339,7 @@ def _plain_post_bwd(s):
     if c["gate"] == "channel":
         dgate = (d * u).sum(0)
     elif c["gate"] == "token":
-        dgate = (d * u).sum(1, keepdim=True)
+        dgate = (d * u).sum(1)
     elif c["gate"] == "full":
         dgate = (d * u).to(s["dh"].dtype)
     if c["norm_y"]:
@@ -395,7 +398,9 @@ def exact(case, seed):
         return d / m.sqrt() - v * ((d * v).sum(1, keepdim=True) / (H * m * m.sqrt()))
 
     def gate():
-        return torch.ones((), dtype=torch.float64, device=s["h"].device) if c["gate"] == "none" else f["gate"]
+        if c["gate"] == "none":
+            return torch.ones((), dtype=torch.float64, device=s["h"].device)
+        return f["gate"].view(T, 1) if c["gate"] == "token" else f["gate"]
 
     def joined(rows, inv, weights):
         out = torch.zeros((T, H), dtype=torch.float64, device=rows.device)
@@ -464,7 +469,7 @@ def exact(case, seed):
     u = unit(f["y"]) * f["w"] if c["norm_y"] else f["y"]
     if c["gate"] != "none":
         out["dgate"] = {"channel": lambda: torch.einsum("th,th->h", d, u), "full": lambda: d * u,
-                        "token": lambda: torch.linalg.vecdot(d, u).unsqueeze(1)}[c["gate"]]()
+                        "token": lambda: torch.linalg.vecdot(d, u)}[c["gate"]]()
     du = d * gate()
     out["dy"] = unit_grad(du * f["w"], f["y"]) if c["norm_y"] else du
     if c["norm_y"]:
