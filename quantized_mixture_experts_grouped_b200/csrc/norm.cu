@@ -11,6 +11,7 @@
 // large batches, by the latency of one launch for small ones. A block holds its rows in registers
 // (8 or 16 values per thread) between its loads and its stores, so no row is read twice.
 #include <algorithm>
+#include <initializer_list>
 #include <type_traits>
 
 #include "norm_back.cuh"
@@ -426,6 +427,11 @@ int check_gate(const char* me, const void* gate, int mode) {
   return MOE_OK;
 }
 
+// Whether an output shares its start with one of the others.
+bool shares(const void* out, std::initializer_list<const void*> others) {
+  return out && std::find(others.begin(), others.end(), out) != others.end();
+}
+
 bool gate16(const void* gate, int mode, int64_t ld, size_t z) {
   if (mode == MOE_GATE_CHANNEL) return rows16(gate, 0, z);
   return mode != MOE_GATE_FULL || rows16(gate, ld, z);
@@ -461,6 +467,13 @@ int check_post(const char* me, const PostArgs& a, int T, int H, int dtype, int f
   if (T > 0 && ((a.h_out == a.h && a.ldho != a.ldh) || a.h_out == a.y ||
                 (a.next && (a.x_next == a.h_out || a.x_next == a.h || a.x_next == a.y))))
     return fail(MOE_ERR_ARG, "%s: outputs overlap", me);
+  // every row reads the vectors; of a gate per value a row reads its own values before it writes them
+  const bool full = a.gate_mode == MOE_GATE_FULL;
+  const void* x = a.next ? a.x_next : nullptr;
+  if (T > 0 && (shares(a.h_out, {a.w, a.w_next}) || shares(x, {a.w, a.w_next}) ||
+                (shares(a.h_out, {a.gate}) && !(full && a.ldho == a.ldg)) ||
+                (shares(x, {a.gate}) && !(full && a.ldx == a.ldg))))
+    return fail(MOE_ERR_ARG, "%s: an output overlaps a weight or the gate", me);
   const size_t z = dtype_size(dtype);
   if (int rc = check_ld(me, "h", a.h, a.ldh, T, H, false)) return rc;
   if (int rc = check_ld(me, "h_out", a.h_out, a.ldho, T, H, true)) return rc;
@@ -557,7 +570,7 @@ MOE_API int moe_norm_pre(const void* h, int64_t h_stride, int dtype, const void*
   const char* me = "moe_norm_pre";
   if (int rc = check_norm(me, T, H, dtype, eps)) return rc;
   if (T > 0 && (!h || !x)) return fail(MOE_ERR_ARG, "%s: null pointer", me);
-  if (T > 0 && x == h) return fail(MOE_ERR_ARG, "%s: x overlaps h", me);
+  if (T > 0 && (x == h || x == w)) return fail(MOE_ERR_ARG, "%s: x overlaps an input", me);
   if (int rc = check_ld(me, "h", h, h_stride, T, H, false)) return rc;
   if (int rc = check_ld(me, "x", x, x_stride, T, H, true)) return rc;
   if (T == 0) return MOE_OK;
@@ -590,7 +603,7 @@ MOE_API int moe_norm_pre_backward(const void* dx, int64_t dx_stride, const void*
   const char* me = "moe_norm_pre_backward";
   if (int rc = check_norm(me, T, H, dtype, eps)) return rc;
   if (T > 0 && (!dx || !h || !dh)) return fail(MOE_ERR_ARG, "%s: null pointer", me);
-  if (T > 0 && (dh == dx || dh == h || (dh == dres && dh_stride != dres_stride)))
+  if (T > 0 && (dh == dx || dh == h || dh == w || (dh == dres && dh_stride != dres_stride)))
     return fail(MOE_ERR_ARG, "%s: dh overlaps an input", me);
   if (int rc = check_ld(me, "dx", dx, dx_stride, T, H, false)) return rc;
   if (int rc = check_ld(me, "h", h, h_stride, T, H, false)) return rc;
@@ -648,8 +661,8 @@ MOE_API int moe_combine_norm_post(const void* yp, int64_t yp_stride, int yp_dtyp
   if (!dtype_size(yp_dtype) || (yp_dtype != dtype && yp_dtype != MOE_DTYPE_F32))
     return fail(MOE_ERR_ARG, "%s: rows of type %d with results of type %d", me, yp_dtype, dtype);
   if (T > 0 && (!inv || !wts)) return fail(MOE_ERR_ARG, "%s: null pointer", me);
-  if (y_out && (y_out == yp || y_out == h || y_out == h_out || y_out == x_next))
-    return fail(MOE_ERR_ARG, "%s: outputs overlap", me);
+  if (shares(y_out, {yp, h, h_out, x_next, w, gate, w_next}))     // written before the gate and the weights are read
+    return fail(MOE_ERR_ARG, "%s: y_out overlaps another tensor", me);
   if (int rc = check_ld(me, "yp", yp, yp_stride, T, H, false)) return rc;
   if (int rc = check_ld(me, "y_out", y_out, y_out_stride, T, H, true)) return rc;
   if (T == 0) return MOE_OK;
@@ -684,6 +697,10 @@ MOE_API int moe_norm_post_backward(const void* dh_out, int64_t dh_out_stride, co
                 (full && dgate && (dgate == dh || dgate == dy || dgate == gate || dgate == y || dgate == dh_out ||
                                    (next && (dgate == h_out || dgate == dx_next))))))
     return fail(MOE_ERR_ARG, "%s: an output overlaps another tensor", me);
+  if (T > 0 && (shares(dh, {w, gate, w_next}) || shares(dy, {w, gate, w_next}) || shares(dgate, {w, w_next})))
+    return fail(MOE_ERR_ARG, "%s: an output overlaps a weight or the gate", me);
+  if (shares(dw, {dw_next, dgate}) || shares(dw_next, {dgate}))
+    return fail(MOE_ERR_ARG, "%s: two gradients share a buffer", me);
   if (int rc = check_ld(me, "dh_out", dh_out, dh_out_stride, T, H, false)) return rc;
   if (int rc = check_ld(me, "y", y, y_stride, T, H, false)) return rc;
   if (int rc = check_ld(me, "dh", dh, dh_stride, T, H, true)) return rc;
