@@ -555,8 +555,8 @@ int launch_combine_rows(const void* yp, int64_t ldy, int ydt, const int32_t* inv
   const bool wide = ydt == MOE_DTYPE_F32;
   const bool eight = vec && k > 4 && (!wide || T <= 256), two = vec && !eight && H > 256;
   const int nt = vec ? row_threads(ceil_div(H, two ? 2 : 1), kRowThreads) : value_threads(H), ny = kRowThreads / nt;
-  const dim3 grid(ceil_div(T, ny), ceil_div(H, 8 * nt * (two ? 2 : 1)));
-  note_launch();
+  // a launch has at most 65535 blocks along the columns: wider rows take one launch per such slice
+  const int cols = 8 * nt * (two ? 2 : 1), slice = 65535 * cols;
   return by_types(ydt, odt, [&](auto* y, auto* o) {
     using YT = std::remove_pointer_t<decltype(y)>;
     using OT = std::remove_pointer_t<decltype(o)>;
@@ -567,9 +567,16 @@ int launch_combine_rows(const void* yp, int64_t ldy, int ydt, const int32_t* inv
                 : !two  ? combine_rows_kernel<YT, OT, 0, 4, 1>
                 : k <= 2 ? combine_rows_kernel<YT, OT, 0, 2, 2>
                          : combine_rows_kernel<YT, OT, 0, sizeof(YT) == 2 ? 4 : 2, 2>;
-    return check_cuda(launch_pdl(kern, grid, dim3(nt, ny), 0, s, static_cast<const YT*>(yp), ldy, inv, wts, T, k, T * k,
-                                 H, static_cast<OT*>(out), ldo),
+    int rc = MOE_OK;
+    for (int64_t c0 = 0; c0 < H && rc == MOE_OK; c0 += slice) {
+      const int h = H - c0 < slice ? (int)(H - c0) : slice;
+      note_launch();
+      rc = check_cuda(launch_pdl(kern, dim3(ceil_div(T, ny), ceil_div(h, cols)), dim3(nt, ny), 0, s,
+                                 static_cast<const YT*>(yp) + c0, ldy, inv, wts, T, k, T * k, h,
+                                 static_cast<OT*>(out) + c0, ldo),
                       "combine_rows_kernel");
+    }
+    return rc;
   });
 }
 

@@ -1,0 +1,38 @@
+"""Calls of the row operators that their documentation allows beside the ordinary ones."""
+import pytest
+import torch
+
+pytestmark = pytest.mark.gpu
+
+q = pytest.importorskip("quantized_mixture_experts_grouped_b200")
+
+
+def room_for(gb):
+    if torch.cuda.mem_get_info()[0] < gb * 2**30:
+        pytest.skip(f"needs {gb} GB of device memory")
+
+
+# rows that take more than 65535 blocks along their columns: single values, words of one chunk per
+# thread (more than four choices in 16 bits), words of two
+@pytest.mark.parametrize("H,k", [(2**27 + 1, 1), (2**27 + 8, 8), (2**28 + 8, 1)])
+def test_very_wide_rows(H, k):
+    """Small whole numbers: every product and sum is exact."""
+    room_for(16)
+    g = torch.Generator(device="cuda").manual_seed(k)
+    yp = torch.randint(-8, 9, (k, H), generator=g, device="cuda", dtype=torch.int8).bfloat16()
+    inv = torch.arange(k, dtype=torch.int32, device="cuda").view(1, k)
+    wts = torch.full((1, k), 0.5, device="cuda")
+    out = torch.full((1, H), 77.0, dtype=torch.bfloat16, device="cuda")
+    total = yp.sum(0, keepdim=True, dtype=torch.float32)
+    q.moe_combine(yp, inv, wts, out)
+    assert torch.equal(out, (total * 0.5).bfloat16())
+    q.moe_dispatch_backward(yp, inv, out)
+    assert torch.equal(out, total.bfloat16())
+    if k == 1:
+        i32 = dict(dtype=torch.int32, device="cuda")
+        xp = torch.full_like(yp, 77.0)
+        q.moe_dispatch(yp, inv, 1, torch.empty(1, **i32), torch.empty(2, **i32), torch.empty(1, **i32),
+                       torch.empty_like(inv), xp)
+        assert torch.equal(xp, yp)
+        q.moe_combine_backward(yp, None, inv, wts, dyp=xp)
+        assert torch.equal(xp, (yp.float() * 0.5).bfloat16())
