@@ -36,3 +36,24 @@ def test_very_wide_rows(H, k):
         assert torch.equal(xp, yp)
         q.moe_combine_backward(yp, None, inv, wts, dyp=xp)
         assert torch.equal(xp, (yp.float() * 0.5).bfloat16())
+
+
+def test_most_tokens():
+    """2^31 - 1 tokens of one value each, several to a block: every one is written."""
+    room_for(48)
+    T = 2**31 - 1
+    row = torch.full((1, 1), 3.0, dtype=torch.bfloat16, device="cuda").expand(T, 1)
+    out = torch.full((T, 1), 77.0, dtype=torch.bfloat16, device="cuda")
+
+    def all_are(value):
+        return all(bool((part == value).all()) for part in out.split(2**28))
+    q.moe_norm_pre(row, None, 1e-5, out)
+    assert all_are(1.0)
+    q.moe_norm_post(row, row, out, 1e-5, alpha=2.0)
+    assert all_are(7.0)
+    zeros = torch.zeros((T, 1), dtype=torch.int32, device="cuda")
+    ones = torch.ones((T, 1), device="cuda")
+    q.moe_combine(row, zeros, ones, out)
+    assert all_are(3.0)
+    q.moe_route_topk_backward(zeros, ones, ones, out)          # 1 * (1 - 1 * 1)
+    assert all_are(0.0)
