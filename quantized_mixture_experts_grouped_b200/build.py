@@ -8,7 +8,8 @@ Each .cu file is compiled to an object under _build/ (in parallel, skipped when 
 then linked into a shared library next to this file. The CUDA runtime is linked statically so
 the library does not depend on the runtime that torch happens to ship. csrc/binding.cpp, the native
 half of the Python binding, becomes the extension module _rows.so (g++, torch's headers), linked
-against that library.
+against that library; _rows.so.stamp beside it records the torch and the interpreter it was built for, and
+it is built again when they change.
 """
 from __future__ import annotations
 
@@ -76,31 +77,57 @@ def build(force: bool = False, verbose: bool = False, extra: list[str] | None = 
     return LIB
 
 
-def _build_binding(force: bool, verbose: bool) -> None:
-    src = os.path.join(CSRC, "binding.cpp")
-    header = os.path.join(INCLUDE, "moe_w4a16.h")
-    if not force and os.path.exists(BINDING) and os.path.getmtime(BINDING) >= max(os.path.getmtime(src),
-                                                                                 os.path.getmtime(header)):
-        return
+def _binding_command(out: str) -> list[str]:
     import sysconfig
 
     import torch
     root = os.path.dirname(torch.__file__)
     cuda = os.environ.get("CUDA_HOME", "/usr/local/cuda")
+    return ["g++", "-std=c++17", "-O2", "-fPIC", "-shared", "-fvisibility=hidden",
+            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", "-I", INCLUDE,
+            "-isystem", sysconfig.get_paths()["include"], "-isystem", os.path.join(root, "include"),
+            "-isystem", os.path.join(root, "include", "torch", "csrc", "api", "include"),
+            "-isystem", os.path.join(cuda, "include"), os.path.join(CSRC, "binding.cpp"), "-o", out, "-L", PKG,
+            "-l:libmoe_w4a16.so", "-L", os.path.join(root, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10_cuda",
+            "-lc10", "-Wl,-rpath,$ORIGIN"]      # torch's own libraries are loaded by then
+
+
+def _binding_stamp() -> str:
+    """What _rows.so is bound to besides its sources: torch, its C++ ABI, the interpreter, the command."""
+    import sysconfig
+
+    import torch
+    return "\n".join([torch.__version__, str(torch.version.git_version), str(sysconfig.get_config_var("SOABI")),
+                      *_binding_command(BINDING)]).replace(ROOT, ".")      # wherever the tree lies
+
+
+def _binding_is_current(binding: str = BINDING, stamp: str | None = None) -> bool:
+    """Whether `binding` is newer than its sources and was built for this torch and this interpreter."""
+    sources = [os.path.join(CSRC, "binding.cpp"), os.path.join(INCLUDE, "moe_w4a16.h")]
+    if not os.path.exists(binding) or any(os.path.getmtime(binding) < os.path.getmtime(s) for s in sources):
+        return False
+    try:
+        with open(binding + ".stamp") as f:
+            return f.read() == (_binding_stamp() if stamp is None else stamp)
+    except OSError:
+        return False
+
+
+def _build_binding(force: bool, verbose: bool) -> None:
+    if not force and _binding_is_current():
+        return
     tmp = BINDING + f".tmp{os.getpid()}"
-    cmd = ["g++", "-std=c++17", "-O2", "-fPIC", "-shared", "-fvisibility=hidden",
-           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", "-I", INCLUDE,
-           "-isystem", sysconfig.get_paths()["include"], "-isystem", os.path.join(root, "include"),
-           "-isystem", os.path.join(root, "include", "torch", "csrc", "api", "include"),
-           "-isystem", os.path.join(cuda, "include"), src, "-o", tmp, "-L", PKG, "-l:libmoe_w4a16.so",
-           "-L", os.path.join(root, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10_cuda", "-lc10",
-           "-Wl,-rpath,$ORIGIN"]      # torch's own libraries are loaded by then
+    cmd = _binding_command(tmp)
     if verbose:
         print(" ".join(cmd), flush=True)
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"g++ failed on binding.cpp:\n{r.stdout}\n{r.stderr}")
+    if os.path.exists(BINDING + ".stamp"):      # none stands beside a module it does not describe
+        os.remove(BINDING + ".stamp")
     os.replace(tmp, BINDING)
+    with open(BINDING + ".stamp", "w") as f:
+        f.write(_binding_stamp())
 
 
 if __name__ == "__main__":
