@@ -93,12 +93,27 @@ def _load() -> ctypes.CDLL:
 
 lib = _load()
 
+
+class _NotLoaded:
+    """Stands for the native binding where it does not load: every row operator's call raises, the calls
+    that go through ctypes (the W4A16 and BF16 layers) work."""
+
+    def __init__(self, why: str):
+        self._why = why
+
+    def __getattr__(self, name):
+        raise ImportError(f"the native binding _rows.so is missing or does not load ({self._why}); build it with "
+                          "`python quantized_mixture_experts_grouped_b200/build.py`")
+
+
 try:
     from . import _rows            # native argument marshalling of the row operators
+    _built_for = getattr(_rows, "built_for", "an earlier one")
+    if _built_for != torch.__version__.split("+")[0]:
+        raise ImportError(f"built for torch {_built_for}, not {torch.__version__}")
+    _rows.set_error(MoeError)
 except ImportError as e:
-    raise ImportError(f"the native binding _rows.so is missing or does not load ({e}); build it with "
-                      "`python quantized_mixture_experts_grouped_b200/build.py`") from e
-_rows.set_error(MoeError)
+    _rows = _NotLoaded(str(e))
 
 
 def _err(rc: int):

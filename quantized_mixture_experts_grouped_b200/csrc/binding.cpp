@@ -8,6 +8,7 @@
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
+#include <torch/version.h>
 
 #include <stdexcept>
 #include <string>
@@ -453,4 +454,12 @@ PyModuleDef module = {PyModuleDef_HEAD_INIT, "_rows", nullptr, -1, methods, null
 
 }  // namespace
 
-PyMODINIT_FUNC PyInit__rows(void) { return PyModule_Create(&module); }
+// built_for: the torch whose tensors this module reads; the package refuses it under another.
+PyMODINIT_FUNC PyInit__rows(void) {
+  PyObject* m = PyModule_Create(&module);
+  if (m && PyModule_AddStringConstant(m, "built_for", TORCH_VERSION) < 0) {
+    Py_DECREF(m);
+    return nullptr;
+  }
+  return m;
+}

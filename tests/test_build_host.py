@@ -1,6 +1,8 @@
-"""When the native binding counts as up to date."""
+"""When the native binding counts as up to date, and what works without it."""
 import importlib.util
 import os
+import subprocess
+import sys
 
 import pytest
 
@@ -43,3 +45,26 @@ def test_binding_is_built_again_for_another_torch(script, tmp_path, monkeypatch)
         assert not script._binding_is_current(str(so))
     assert script._binding_is_current(str(so))
 
+
+
+@pytest.mark.parametrize("broken", ["sys.modules[name + '._rows'] = None",
+                                    "import torch; torch.__version__ = '0.0.1+cpu'"])
+def test_layer_calls_without_the_native_binding(broken):
+    """Where _rows.so is missing or built for another torch, the package imports and the calls through
+    ctypes work; a row operator's call raises and says what to do."""
+    code = f"""
+import sys
+name = "quantized_mixture_experts_grouped_b200"
+{broken}
+import quantized_mixture_experts_grouped_b200 as q
+assert q.moe_packed_bytes(256, 256) == 256 * 256 // 2 and q.moe_workspace_bytes(4, 256, 128, 8, 2) > 0
+assert q.moe_norm_workspace_bytes(4, 8) > 0
+try:
+    q.moe_norm_pre(None, None, 1e-5, None)
+except ImportError as e:
+    assert "build.py" in str(e)
+else:
+    raise AssertionError("the call did not raise")
+"""
+    r = subprocess.run([sys.executable, "-c", code], cwd=ROOT, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0, r.stderr[-2000:]
