@@ -40,7 +40,7 @@ inline int check_launch(const char* what) {
 }
 
 inline size_t align_up(size_t v, size_t a) { return (v + a - 1) / a * a; }
-inline int ceil_div(int a, int b) { return a / b + (a % b != 0); }      // a >= 0; a + b may not fit an int
+inline int ceil_div(int a, int b) { return (a + b - 1) / b; }
 
 // ---- workspace layout (all offsets 256-byte aligned) ----
 struct WsLayout {

@@ -346,7 +346,7 @@ Shape shape_of(int H, bool words) {
   }
   const int nt = row_threads(H, 1024);
   if (H <= 8 * nt) return {nt, 1, 1};
-  return {row_threads(ceil_div(H, 2), 1024), 2, 1};
+  return {row_threads(parts_of(H, 2), 1024), 2, 1};
 }
 // Forward, up to 4096 values: 256 threads, with two chunks per thread (half as many exchanges per row,
 // twice the loads in flight per thread: T = 2048, H = 2048, bf16, post with next norm 6.2 us against
@@ -359,7 +359,7 @@ Shape shape_forward(int rows, int H, bool words) {
     return {nt, nc, nt > 256 ? 1 : 256 / nt};
   }
   if (H > 4096 || (H > 2048 && rows <= 256)) return shape_of(H, true);
-  const int nc = H <= 256 || (H <= 2048 && rows <= 256) ? 1 : 2, nt = row_threads(ceil_div(H, nc), 256);
+  const int nc = H <= 256 || (H <= 2048 && rows <= 256) ? 1 : 2, nt = row_threads(parts_of(H, nc), 256);
   return {nt, nc, 256 / nt < kBlockRows ? 256 / nt : kBlockRows};
 }
 // Calls f(threads, chunks) as integral constants for the forward shape of single values.
@@ -455,7 +455,7 @@ int launch_post(const PostArgs& a, int rows, bool vec, cudaStream_t s) {
   };
   auto kern = vec ? words() : by_values(sh, values);
   note_launch();
-  return check_cuda(launch_pdl(kern, dim3(ceil_div(rows, sh.ny)), dim3(sh.nt, sh.ny), 0, s, a), "norm_post_kernel");
+  return check_cuda(launch_pdl(kern, dim3(parts_of(rows, sh.ny)), dim3(sh.nt, sh.ny), 0, s, a), "norm_post_kernel");
 }
 
 // Checks common to moe_norm_post and moe_combine_norm_post; *vec receives whether rows move as words.
@@ -521,7 +521,7 @@ int launch_back(const char* me, BackArgs& a, int dtype, bool vec, void* ws, size
   // the launches counts).
   int blocks = back_blocks(a.T, a.H, any && per_sm > 8 ? 8 : per_sm);
   const bool one = a.T <= 2 || (vec && a.T <= 4 && a.T * a.H <= 6144);
-  if (any) blocks = one ? 1 : std::min(blocks, std::max(norm_sms(), ceil_div(a.T, 2)));
+  if (any) blocks = one ? 1 : std::min(blocks, std::max(norm_sms(), parts_of(a.T, 2)));
   a.part_ld = part_stride(a.H);
   if (any) {                       // asked for whether or not this call's size uses it
     const size_t need = norm_ws(a.T, a.H);
@@ -547,7 +547,7 @@ int launch_back(const char* me, BackArgs& a, int dtype, bool vec, void* ws, size
   }
   const bool many = blocks > 5 * 128;
   note_launch();
-  return check_cuda(launch_pdl(many ? norm_sums_kernel<2> : norm_sums_kernel<8>, dim3(ceil_div(a.H, many ? 8 : 32), n),
+  return check_cuda(launch_pdl(many ? norm_sums_kernel<2> : norm_sums_kernel<8>, dim3(parts_of(a.H, many ? 8 : 32), n),
                                dim3(1024), 0, s, (const float*)a.part, blocks, a.H, a.part_ld, asked),
                     "norm_sums_kernel");
 }
@@ -589,7 +589,7 @@ MOE_API int moe_norm_pre(const void* h, int64_t h_stride, int dtype, const void*
       return norm_pre_kernel<T_, N, decltype(c)::value, N <= 256 ? 256 : N>;
     };
     auto kern = vec ? words() : by_values(sh, values);
-    return check_cuda(launch_pdl(kern, dim3(ceil_div(T, sh.ny)), dim3(sh.nt, sh.ny), 0,
+    return check_cuda(launch_pdl(kern, dim3(parts_of(T, sh.ny)), dim3(sh.nt, sh.ny), 0,
                                  reinterpret_cast<cudaStream_t>(stream), static_cast<const T_*>(h), h_stride,
                                  static_cast<const T_*>(w), eps, T, H, static_cast<T_*>(x), x_stride),
                       "norm_pre_kernel");

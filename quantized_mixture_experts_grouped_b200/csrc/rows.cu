@@ -554,7 +554,7 @@ int launch_combine_rows(const void* yp, int64_t ldy, int ydt, const int32_t* inv
   // Single values: one chunk of four, of eight for few tokens. Narrow rows share a block.
   const bool wide = ydt == MOE_DTYPE_F32;
   const bool eight = vec && k > 4 && (!wide || T <= 256), two = vec && !eight && H > 256;
-  const int nt = vec ? row_threads(ceil_div(H, two ? 2 : 1), kRowThreads) : value_threads(H), ny = kRowThreads / nt;
+  const int nt = vec ? row_threads(parts_of(H, two ? 2 : 1), kRowThreads) : value_threads(H), ny = kRowThreads / nt;
   // a launch has at most 65535 blocks along the columns: wider rows take one launch per such slice
   const int cols = 8 * nt * (two ? 2 : 1), slice = 65535 * cols;
   return by_types(ydt, odt, [&](auto* y, auto* o) {
@@ -571,7 +571,7 @@ int launch_combine_rows(const void* yp, int64_t ldy, int ydt, const int32_t* inv
     for (int64_t c0 = 0; c0 < H && rc == MOE_OK; c0 += slice) {
       const int h = H - c0 < slice ? (int)(H - c0) : slice;
       note_launch();
-      rc = check_cuda(launch_pdl(kern, dim3(ceil_div(T, ny), ceil_div(h, cols)), dim3(nt, ny), 0, s,
+      rc = check_cuda(launch_pdl(kern, dim3(parts_of(T, ny), parts_of(h, cols)), dim3(nt, ny), 0, s,
                                  static_cast<const YT*>(yp) + c0, ldy, inv, wts, T, k, T * k, h,
                                  static_cast<OT*>(out) + c0, ldo),
                       "combine_rows_kernel");
@@ -698,7 +698,7 @@ MOE_API int moe_combine_backward(const void* dout, int64_t dout_stride, int dout
                 : G == 1 ? form(std::integral_constant<int, 1>())
                 : G == 2 ? form(std::integral_constant<int, 2>())
                          : form(std::integral_constant<int, 4>());
-    const dim3 grid(G ? T * ceil_div(k, G) : T), block(vec ? row_threads(H, kRowThreads) : value_threads(H));
+    const dim3 grid(G ? T * parts_of(k, G) : T), block(vec ? row_threads(H, kRowThreads) : value_threads(H));
     return check_cuda(launch_pdl(kern, grid, block, 0, reinterpret_cast<cudaStream_t>(stream), static_cast<const OT*>(dout), dout_stride,
                                  static_cast<const YT*>(yp), yp_stride, inv, wts, k, T * k, H, static_cast<YT*>(dyp),
                                  dyp_stride, dwts),
@@ -721,7 +721,7 @@ MOE_API int moe_route_topk_backward(const int32_t* idx, const float* wts, const 
     using LT = std::remove_pointer_t<decltype(l)>;
     const bool vec = E % 8 == 0 && rows16(dlogits, dlogits_stride, sizeof(LT));
     auto kern = vec ? route_backward_kernel<LT, true> : route_backward_kernel<LT, false>;
-    return check_cuda(launch_pdl(kern, dim3(ceil_div(T, kRouterWarps)), dim3(32 * kRouterWarps), 0,
+    return check_cuda(launch_pdl(kern, dim3(parts_of(T, kRouterWarps)), dim3(32 * kRouterWarps), 0,
                                  reinterpret_cast<cudaStream_t>(stream), idx, wts, dwts, T, E, k,
                                  static_cast<LT*>(dlogits), dlogits_stride),
                       "route_backward_kernel");

@@ -276,6 +276,8 @@ __device__ __forceinline__ void weighted_rows(const T* rows, int64_t ld, const i
 }
 
 // ---- host side ----
+// Parts of at most `per` that n >= 0 things take; n + per need not fit an int (2^31 - 1 tokens are allowed).
+inline int parts_of(int n, int per) { return n / per + (n % per != 0); }
 // moe_dispatch without its checks; `size` bytes per value, strides in values (rows.cu). Also the grouped
 // layer path's first step.
 int launch_dispatch(const void* x, int64_t ldx, size_t size, const int32_t* idx, int T, int H, int E, int k,
@@ -300,7 +302,7 @@ auto by_width(int H, F f) {
 }
 // Threads of a block that covers H values in chunks of 8, at most `most`.
 inline int row_threads(int H, int most) {
-  const int t = (ceil_div(H, 8) + 31) / 32 * 32;
+  const int t = (parts_of(H, 8) + 31) / 32 * 32;
   return t < most ? t : most;
 }
 
