@@ -69,7 +69,8 @@ def on_device(got, want, arith, what):
 # from the ring, words and single values of one and two chunks above it
 MANY = [(3000, 512, 0, "bf16 f16 f32"), (3001, 264, 8, "bf16 f16 f32"), (2500, 264, 1, "bf16 f16 f32"),
         (700, 4096, 0, "bf16 f32"), (700, 1031, 0, "bf16 f32"), (700, 4095, 0, "f16"),
-        (4, 1536, 0, "bf16 f32"), (2, 4096, 1, "f16"), (500, 5000, 0, "bf16 f32"), (500, 5000, 1, "bf16 f32"), (400, 12544, 0, "bf16 f32"), (400, 12543, 0, "f16")]
+        (4, 1536, 0, "bf16 f32"), (2, 4096, 1, "f16"), (500, 5000, 0, "bf16 f32"),
+        (500, 5000, 1, "bf16 f32"), (400, 12544, 0, "bf16 f32"), (400, 12543, 0, "f16")]
 
 
 @pytest.mark.parametrize("norm_y,gate,nxt", CASES)

@@ -87,3 +87,123 @@ def test_pre_output_overlaps(other):
 def test_pre_gradient_overlaps(change):
     base = dict(buffers("dx h w dres dh dw ws"), lddx=8, ldh=8, dt=BF16, eps=1e-5, T=4, H=8, ldr=8, lddh=8, wb=1 << 30)
     refused("moe_norm_pre_backward", PRE_BACK, base, change, ARG, "overlap")
+
+
+DISPATCH = "x ldx dt idx T H E k counts offsets perm inv xp ldp"
+DISPATCH_BASE = dict(buffers("x idx counts offsets perm inv xp"), ldx=8, dt=BF16, T=4, H=8, E=4, k=2, ldp=8)
+
+
+@pytest.mark.parametrize("change,code,says", [
+    *[({n: N}, ARG, "null pointer") for n in ("x", "idx", "counts", "offsets", "perm", "inv", "xp")],
+    (dict(T=0, counts=N), ARG, "null pointer"), (dict(T=0, offsets=N), ARG, "null pointer"),
+    (dict(T=-1), ARG, "bad sizes"), (dict(H=0), ARG, "bad sizes"), (dict(k=0), ARG, "bad sizes"),
+    (dict(E=0), ARG, "E=0"), (dict(E=257), SHAPE, "E=257"), (dict(dt=3), ARG, "type 3"), (dict(dt=-1), ARG, "type -1"),
+    (dict(ldx=-8), ARG, "row stride -8 of x "), (dict(ldp=7), ARG, "row stride 7 of xp"),
+    (dict(ldp=0), ARG, "row stride 0 of xp"), (dict(xp="x"), ARG, "xp overlaps x"),
+    (dict(T=1 << 30, k=4), SHAPE, "T*k"), (dict(H=(1 << 30) + 1, ldp=1 << 31), SHAPE, "2^30"),
+    *[({n: "idx"}, ARG, "index outputs overlap") for n in ("counts", "offsets", "perm", "inv")],
+    (dict(perm="inv"), ARG, "index outputs overlap")])
+def test_dispatch(change, code, says):
+    refused("moe_dispatch", DISPATCH, DISPATCH_BASE, change, code, says)
+
+
+@pytest.mark.parametrize("change,code,says", [
+    *[({n: N}, ARG, "null pointer") for n in ("dxp", "inv", "dx")],
+    (dict(T=-1), ARG, "bad sizes"), (dict(H=0), ARG, "bad sizes"), (dict(k=0), ARG, "bad sizes"),
+    (dict(dt=5), ARG, "type 5"), (dict(dx="dxp"), ARG, "dx overlaps dxp"), (dict(ldxp=-1), ARG, "of dxp"),
+    (dict(ldx=3), ARG, "row stride 3 of dx "), (dict(T=1 << 30, k=2), SHAPE, "T*k"),
+    (dict(H=(1 << 30) + 1, ldx=1 << 31), SHAPE, "2^30")])
+def test_dispatch_backward(change, code, says):
+    base = dict(buffers("dxp inv dx"), ldxp=8, dt=F16, T=4, H=8, k=2, ldx=8)
+    refused("moe_dispatch_backward", "dxp ldxp dt inv T H k dx ldx", base, change, code, says)
+
+
+@pytest.mark.parametrize("change,code,says", [
+    *[({n: N}, ARG, "null pointer") for n in ("yp", "inv", "wts", "out")],
+    (dict(T=-2), ARG, "bad sizes"), (dict(H=0), ARG, "bad sizes"), (dict(k=0), ARG, "bad sizes"),
+    (dict(ydt=9), ARG, "unknown type 9"), (dict(odt=9), ARG, "unknown type 9"),
+    (dict(ydt=BF16, odt=F32), ARG, "results of type"), (dict(ydt=BF16, odt=F16), ARG, "results of type"),
+    (dict(out="yp"), ARG, "out overlaps yp"), (dict(ldyp=-1), ARG, "of yp"), (dict(ldo=7), ARG, "row stride 7 of out"),
+    (dict(T=1 << 30, k=2), SHAPE, "T*k"), (dict(H=(1 << 30) + 1, ldo=1 << 31), SHAPE, "2^30")])
+def test_combine(change, code, says):
+    base = dict(buffers("yp inv wts out"), ldyp=8, ydt=F32, T=4, H=8, k=2, ldo=8, odt=BF16)
+    refused("moe_combine", "yp ldyp ydt inv wts T H k out ldo odt", base, change, code, says)
+
+
+@pytest.mark.parametrize("change,code,says", [
+    *[({n: N}, ARG, "null pointer") for n in ("dout", "yp", "inv", "wts")],
+    (dict(dyp=N, dwts=N), ARG, "both null"), (dict(dyp="yp"), ARG, "dyp overlaps"),
+    (dict(dyp="dout"), ARG, "dyp overlaps"), (dict(T=-1), ARG, "bad sizes"), (dict(H=0), ARG, "bad sizes"), (dict(k=0), ARG, "bad sizes"),
+    (dict(ydt=7), ARG, "unknown type 7"), (dict(ddt=7), ARG, "unknown type 7"),
+    (dict(ydt=F16, ddt=BF16), ARG, "results of type"), (dict(lddout=-1), ARG, "of dout"), (dict(ldyp=-1), ARG, "of yp"),
+    (dict(lddyp=4), ARG, "row stride 4 of dyp"), (dict(T=1 << 30, k=2), SHAPE, "T*k"),
+    (dict(H=(1 << 30) + 1, lddyp=1 << 31), SHAPE, "2^30")])
+def test_combine_backward(change, code, says):
+    base = dict(buffers("dout yp inv wts dyp dwts"), lddout=8, ddt=BF16, ldyp=8, ydt=BF16, T=4, H=8, k=2, lddyp=8)
+    order = "dout lddout ddt yp ldyp ydt inv wts T H k dyp lddyp dwts"
+    refused("moe_combine_backward", order, base, change, code, says)
+
+
+@pytest.mark.parametrize("change,code,says", [
+    *[({n: N}, ARG, "null pointer") for n in ("idx", "wts", "dwts", "dl")],
+    (dict(T=-1), ARG, "bad sizes"), (dict(k=0), ARG, "bad sizes"), (dict(k=9), ARG, "bad sizes"),
+    (dict(E=300, ld=300), SHAPE, "E=300"), (dict(ld=7), ARG, "row stride 7 of dlogits"), (dict(dt=4), ARG, "type 4"),
+    (dict(T=1 << 30), SHAPE, "T*k")])
+def test_router_backward(change, code, says):
+    base = dict(buffers("idx wts dwts dl"), T=4, E=8, k=2, ld=8, dt=F32)
+    refused("moe_route_topk_backward", "idx wts dwts T E k dl ld dt", base, change, code, says)
+
+
+NORM_SIZES = [(dict(T=-1), ARG, "bad sizes"), (dict(H=0), ARG, "bad sizes"), (dict(H=16385), SHAPE, "H=16385"),
+              (dict(dt=3), ARG, "type 3"), (dict(eps=0.0), ARG, "eps"), (dict(eps=-1.0), ARG, "eps"),
+              (dict(eps=float("nan")), ARG, "eps"), (dict(eps=float("inf")), ARG, "eps")]
+
+
+@pytest.mark.parametrize("change,code,says", [
+    *NORM_SIZES, (dict(h=N), ARG, "null pointer"), (dict(x=N), ARG, "null pointer"), (dict(ldh=-1), ARG, "of h "),
+    (dict(ldx=4), ARG, "row stride 4 of x")])
+def test_pre(change, code, says):
+    base = dict(buffers("h w x"), ldh=8, dt=BF16, eps=1e-5, T=4, H=8, ldx=8)
+    refused("moe_norm_pre", PRE, base, change, code, says)
+
+
+@pytest.mark.parametrize("change,code,says", [
+    *NORM_SIZES, *[({n: N}, ARG, "null pointer") for n in ("dx", "h", "dh")], (dict(lddx=-1), ARG, "of dx"),
+    (dict(ldh=-1), ARG, "of h "), (dict(ldr=-1), ARG, "of dres"), (dict(lddh=2), ARG, "row stride 2 of dh"),
+    (dict(ws=N), ARG, "workspace of 0"), (dict(wb=16), ARG, "workspace of 16"),
+    (dict(ws=ctypes.c_void_p((1 << 40) + 1)), ARG, "aligned")])
+def test_pre_backward(change, code, says):
+    base = dict(buffers("dx h w dres dh dw ws"), lddx=8, ldh=8, dt=BF16, eps=1e-5, T=4, H=8, ldr=8, lddh=8, wb=1 << 30)
+    refused("moe_norm_pre_backward", PRE_BACK, base, change, code, says)
+
+
+@pytest.mark.parametrize("change,code,says", [
+    *NORM_SIZES, *[({n: N}, ARG, "null pointer") for n in ("y", "h", "ho", "xn")],
+    (dict(flags=4), ARG, "unknown flags 4"), (dict(mode=4), ARG, "gate mode 4"), (dict(mode=-1), ARG, "gate mode -1"),
+    (dict(mode=0), ARG, "do not go together"), (dict(gate=N), ARG, "do not go together"), (dict(ldy=-1), ARG, "of y "),
+    (dict(ldh=-1), ARG, "of h "), (dict(ldho=7), ARG, "row stride 7 of h_out"), (dict(ldx=7), ARG, "of x_next"),
+    (dict(ldg=-1), ARG, "of gate")])
+def test_post(change, code, says):
+    refused("moe_norm_post", POST, POST_BASE, change, code, says)
+
+
+@pytest.mark.parametrize("change,code,says", [
+    *NORM_SIZES, *[({n: N}, ARG, "null pointer") for n in ("yp", "inv", "wts", "h", "ho", "xn")],
+    (dict(k=0), ARG, "k=0"), (dict(T=1 << 30), SHAPE, "T*k"), (dict(ydt=F16), ARG, "results of type"),
+    (dict(ydt=7), ARG, "of type 7"), (dict(dt=F32, ydt=BF16), ARG, "results of type"), (dict(ldyp=-1), ARG, "of yp"),
+    (dict(ldyo=7), ARG, "row stride 7 of y_out"), (dict(ldho=7), ARG, "of h_out"), (dict(ho="yp"), ARG, "overlap")])
+def test_fused(change, code, says):
+    refused("moe_combine_norm_post", FUSED, FUSED_BASE, change, code, says)
+
+
+@pytest.mark.parametrize("change,code,says", [
+    *NORM_SIZES, *[({n: N}, ARG, "null pointer") for n in ("dho", "y", "ho", "dx", "dh", "dy")],
+    (dict(flags=8), ARG, "unknown flags 8"), (dict(mode=4), ARG, "gate mode 4"),
+    (dict(gate=N), ARG, "do not go together"), (dict(flags=2), ARG, "gradient asked"), (dict(flags=1), ARG, "gradient asked"),
+    (dict(mode=0, gate=N), ARG, "gradient asked"), (dict(lddho=-1), ARG, "of dh_out"), (dict(ldy=-1), ARG, "of y "),
+    (dict(lddh=7), ARG, "row stride 7 of dh "), (dict(lddy=7), ARG, "of dy"), (dict(ldho=-1), ARG, "of h_out"),
+    (dict(lddx=-1), ARG, "of dx_next"), (dict(ldg=-1), ARG, "of gate"), (dict(lddg=7), ARG, "of dgate"),
+    (dict(ws=N), ARG, "workspace of 0"), (dict(wb=64), ARG, "workspace of 64"),
+    (dict(ws=ctypes.c_void_p((1 << 40) + 128)), ARG, "aligned")])
+def test_post_backward(change, code, says):
+    refused("moe_norm_post_backward", BACK, BACK_BASE, change, code, says)
