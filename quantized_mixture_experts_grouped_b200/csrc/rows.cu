@@ -391,16 +391,18 @@ __global__ void __launch_bounds__(kRowThreads, 4)
 }
 
 // The same with a block per token and group of G choices: groups do not wait for one another, and dout's
-// row, read once per group, comes from L2 after the first. One choice in a group where latency counts
-// (T = 1, k = 8, H = 2048, bf16: 1.7 us against 2.8 with a block per token; 512 pairs: 2.3 against 3.1;
-// 1024: 3.3 against 3.2, fp32 4.3 against 5.0; 2048: 4.8 against 4.0) or where one or two wide rows stream (T = 8192, k = 2, H = 2048: 36 against 38
-// with two and 50 with a block per token). Rows moved value by value are bound by their single loads and
-// stores, of which a group shares dout's (T = 2048, k = 8, H = 2048, bf16: 48, 42, 36, 42 us with 1, 2, 4,
-// 8; H = 1031: 32, 26, 22; T = 4096, H = 255: 34, 17, 9.1, 8.4). Words of fp32 take two (T = 2048, k = 8,
-// H = 2048: 51, 45, 46, 51 against 54 with a block per token; k = 4: 27, 24, 25, 29 against 30; T = 4096,
-// k = 8, H = 512: 35, 23, 23, 25 against 29, but H = 128: 34, 17, 8.9, 6.1 against 8.1), 16-bit words a
-// block per token (T = 2048, k = 8: 35, 37, 32, 43 against 27) unless there are two narrow ones (T = 8192,
-// H = 512: 17, 8.9 against 10).
+// row, read once per group, comes from L2 after the first. Which form a call takes, with the microseconds
+// of groups of 1 / 2 / 4 / 8 and of a block per token (bf16 rows, H = 2048, unless it says otherwise):
+//   up to 1024 pairs, where latency counts, one choice: T = 1, k = 8: 1.7 against 2.8 per token; 512 pairs:
+//     2.3 against 3.1; 1024: 3.3 against 3.2 (fp32 4.3 against 5.0); 2048: 4.8 against 4.0
+//   one choice, and two of words wider than 1024, one: T = 8192, k = 2: 36 / 38 against 50
+//   single values, bound by their loads and stores, of which a group shares dout's, four (two of two):
+//     T = 2048, k = 8: 48 / 42 / 36 / 42; H = 1031: 32 / 26 / 22; T = 4096, H = 255: 34 / 17 / 9.1 / 8.4
+//   two narrow choices of words, two: T = 8192, H = 512: 17 / 8.9 against 10
+//   fp32 words from 512 values on, two: T = 2048, k = 8: 51 / 45 / 46 / 51 against 54; k = 4: 27 / 24 / 25 /
+//     29 against 30; T = 4096, k = 8, H = 512: 35 / 23 / 23 / 25 against 29 (H = 128: 34 / 17 / 8.9 / 6.1
+//     against 8.1)
+//   other words, a block per token: T = 2048, k = 8: 35 / 37 / 32 / 43 against 27
 template <typename YT, typename OT, int NT, int G>
 __global__ void __launch_bounds__(kRowThreads)
     combine_group_backward_kernel(const OT* __restrict__ dout, int64_t ldo, const YT* __restrict__ yp, int64_t ldy,
@@ -691,17 +693,20 @@ MOE_API int moe_combine_backward(const void* dout, int64_t dout_stride, int dout
                   : !vec                                                   ? (k == 2 ? 2 : 4)
                   : k == 2 || (sizeof(YT) == 4 && H >= 512)                ? 2 : 0;
     auto form = [&](auto g) {
-      auto by_nt = [](auto n) { return combine_group_backward_kernel<YT, OT, decltype(n)::value, decltype(g)::value>; };
-      return vec ? by_nt(std::integral_constant<int, 0>()) : by_width<32, 128, 256>(H, by_nt);
+      constexpr int N = decltype(g)::value;
+      auto by_nt = [](auto n) { return combine_group_backward_kernel<YT, OT, decltype(n)::value, N>; };
+      if constexpr (N < 4)      // groups of four are for single values alone
+        if (vec) return by_nt(std::integral_constant<int, 0>());
+      return by_width<32, 128, 256>(H, by_nt);
     };
     auto kern = G == 0   ? combine_backward_kernel<YT, OT>
                 : G == 1 ? form(std::integral_constant<int, 1>())
                 : G == 2 ? form(std::integral_constant<int, 2>())
                          : form(std::integral_constant<int, 4>());
     const dim3 grid(G ? T * parts_of(k, G) : T), block(vec ? row_threads(H, kRowThreads) : value_threads(H));
-    return check_cuda(launch_pdl(kern, grid, block, 0, reinterpret_cast<cudaStream_t>(stream), static_cast<const OT*>(dout), dout_stride,
-                                 static_cast<const YT*>(yp), yp_stride, inv, wts, k, T * k, H, static_cast<YT*>(dyp),
-                                 dyp_stride, dwts),
+    return check_cuda(launch_pdl(kern, grid, block, 0, reinterpret_cast<cudaStream_t>(stream),
+                                 static_cast<const OT*>(dout), dout_stride, static_cast<const YT*>(yp), yp_stride, inv,
+                                 wts, k, T * k, H, static_cast<YT*>(dyp), dyp_stride, dwts),
                       "combine_backward_kernel");
   });
 }
