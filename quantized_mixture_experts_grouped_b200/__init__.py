@@ -299,8 +299,8 @@ def moe_norm_post_backward(dh_out, y, dh, dy, eps: float, alpha: float = 1.0, no
                            gate=None, dgate=None, h_out=None, w_next=None, dx_next=None, dw_next=None, ws=None,
                            stream=None):
     """Gradients of moe_norm_post: dh, dy, and where given dw, dw_next (fp32 [H]) and dgate (fp32 [H], fp32
-    [T][1] or [T], or rows, as the gate is). With dx_next given, h_out is the forward's output. Gradients of vectors need
-    ws, a workspace of moe_norm_workspace_bytes. dh may be dh_out."""
+    [T][1] or [T], or rows, as the gate is). With dx_next given, h_out is the forward's output. Gradients of
+    vectors need ws, a workspace of moe_norm_workspace_bytes. dh may be dh_out."""
     _rows.norm_post_backward(dh_out, y, dh, dy, eps, alpha, norm_y, w, dw, gate, dgate, h_out, w_next, dx_next,
                              dw_next, ws, stream)
 

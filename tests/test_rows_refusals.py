@@ -133,7 +133,8 @@ def test_combine(change, code, says):
 @pytest.mark.parametrize("change,code,says", [
     *[({n: N}, ARG, "null pointer") for n in ("dout", "yp", "inv", "wts")],
     (dict(dyp=N, dwts=N), ARG, "both null"), (dict(dyp="yp"), ARG, "dyp overlaps"),
-    (dict(dyp="dout"), ARG, "dyp overlaps"), (dict(T=-1), ARG, "bad sizes"), (dict(H=0), ARG, "bad sizes"), (dict(k=0), ARG, "bad sizes"),
+    (dict(dyp="dout"), ARG, "dyp overlaps"), (dict(T=-1), ARG, "bad sizes"), (dict(H=0), ARG, "bad sizes"),
+    (dict(k=0), ARG, "bad sizes"),
     (dict(ydt=7), ARG, "unknown type 7"), (dict(ddt=7), ARG, "unknown type 7"),
     (dict(ydt=F16, ddt=BF16), ARG, "results of type"), (dict(lddout=-1), ARG, "of dout"), (dict(ldyp=-1), ARG, "of yp"),
     (dict(lddyp=4), ARG, "row stride 4 of dyp"), (dict(T=1 << 30, k=2), SHAPE, "T*k"),
@@ -199,7 +200,8 @@ def test_fused(change, code, says):
 @pytest.mark.parametrize("change,code,says", [
     *NORM_SIZES, *[({n: N}, ARG, "null pointer") for n in ("dho", "y", "ho", "dx", "dh", "dy")],
     (dict(flags=8), ARG, "unknown flags 8"), (dict(mode=4), ARG, "gate mode 4"),
-    (dict(gate=N), ARG, "do not go together"), (dict(flags=2), ARG, "gradient asked"), (dict(flags=1), ARG, "gradient asked"),
+    (dict(gate=N), ARG, "do not go together"), (dict(flags=2), ARG, "gradient asked"),
+    (dict(flags=1), ARG, "gradient asked"),
     (dict(mode=0, gate=N), ARG, "gradient asked"), (dict(lddho=-1), ARG, "of dh_out"), (dict(ldy=-1), ARG, "of y "),
     (dict(lddh=7), ARG, "row stride 7 of dh "), (dict(lddy=7), ARG, "of dy"), (dict(ldho=-1), ARG, "of h_out"),
     (dict(lddx=-1), ARG, "of dx_next"), (dict(ldg=-1), ARG, "of gate"), (dict(lddg=7), ARG, "of dgate"),
