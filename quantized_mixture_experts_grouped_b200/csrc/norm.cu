@@ -99,7 +99,8 @@ __global__ void __launch_bounds__(MAXT) norm_pre_kernel(const T* __restrict__ h,
 
 // YT: type of the rows y comes from (fused: y is the combine of its token's rows). h_out may be h:
 // a thread reads its values of the row before it writes them, and no other thread reads them.
-// FUSED: the choices read at a time, 0 for rows that are y itself.
+// FUSED: the choices read at a time, 0 for rows that are y itself. Eight blocks per SM cost the form of
+// words with one chunk 4 to 8 bytes of spill per thread, four the fused forms of single values 44 to 152.
 template <typename T, typename YT, int FUSED, int NT, int NC, int MAXT>
 __global__ void __launch_bounds__(MAXT, MAXT == 256 ? (NC == 2 || NT > 0 ? 4 : FUSED ? 1 : 8) : 1)
     norm_post_kernel(const PostArgs a) {
@@ -159,8 +160,11 @@ __global__ void __launch_bounds__(MAXT, MAXT == 256 ? (NC == 2 || NT > 0 ? 4 : F
 
 // The gradient for rows too wide for the ring (norm_ring.cuh; above 4096 values). One block takes rows
 // blockIdx.x, + gridDim.x, ...; every thread keeps the same columns, so the sums over the tokens stay
-// in its registers (above 8192 values spilled to local memory) and leave once per block, as partial
-// sums that norm_sums_kernel adds in block order (no atomics: bit-identical run to run).
+// with it and leave once per block, as partial sums that norm_sums_kernel adds in block order (no atomics:
+// bit-identical run to run). 1024 threads leave 64 registers for three such sums, four tensors and the
+// row's values: every form spills, 296 to 460 bytes per thread with one chunk (up to 8192 values), 800 to
+// 1472 with two, and a row's loads wait for the sums of the row before. Right, not fast: T = 4096, bf16, both
+// norms: 208 us at H = 7168 and 1240 at 16384, where the bytes take 54 and 123.
 template <typename T, int NT, int NC>
 __global__ void __launch_bounds__(1024) norm_backward_kernel(const BackArgs a) {
   __shared__ float buf[2][32 * 4];
@@ -441,8 +445,9 @@ template <typename T, typename YT, bool FUSED>
 int launch_post(const PostArgs& a, int rows, bool vec, cudaStream_t s) {
   const Shape sh = shape_forward(rows, a.H, vec);
   // choices read at a time: eight with one chunk per thread, for few tokens; two with two chunks, which
-  // leaves room for four blocks per SM (T = 2048, k = 8, H = 2048, bf16: 17.2 us, with four at a time in
-  // two blocks 22.3, and moe_combine and moe_norm_post one after the other 20.3)
+  // leaves room for four blocks per SM (T = 2048, k = 8, H = 2048, bf16, on one input, partly in L2: 17.2 us,
+  // with four at a time in two blocks 22.3, and moe_combine and moe_norm_post one after the other 20.3; on
+  // inputs that change 22.0 against 23.1 one after the other)
   constexpr int F8 = FUSED ? 8 : 0, F4 = FUSED ? 4 : 0, F2_ = FUSED ? 2 : 0;
   auto words = [&]() {
     if (sh.nt * sh.ny <= 256)

@@ -1,4 +1,5 @@
-// The gradient of the norms around a block for rows of 16-byte words (see norm.cu for the formulas).
+// The gradient of the norms around a block (see norm.cu for the formulas): its arguments, and the launch of
+// the ring form, for rows of up to 4096 values.
 #pragma once
 
 #include "rows.cuh"

@@ -341,7 +341,8 @@ __global__ void __launch_bounds__(kRowThreads, 4)
       F2 d[4];
       load8<0>(dout + t * ldo, c, nt, tid, H, d);
       // four choices' words at a time and four blocks per SM: T = 2048, k = 8, H = 2048 took 54 us for
-      // the whole gradient with eight and three, 49 with four and five (spills), 44 like this
+      // this and moe_dispatch_backward with eight and three, 49 with four and five (spills), 44 like this
+      // (fp32 rows spill 24 bytes)
       constexpr int B = 4;
 #pragma unroll
       for (int b0 = 0; b0 < kDots; b0 += B) {
@@ -392,17 +393,19 @@ __global__ void __launch_bounds__(kRowThreads, 4)
 
 // The same with a block per token and group of G choices: groups do not wait for one another, and dout's
 // row, read once per group, comes from L2 after the first. Which form a call takes, with the microseconds
-// of groups of 1 / 2 / 4 / 8 and of a block per token (bf16 rows, H = 2048, unless it says otherwise):
-//   up to 1024 pairs, where latency counts, one choice: T = 1, k = 8: 1.7 against 2.8 per token; 512 pairs:
-//     2.3 against 3.1; 1024: 3.3 against 3.2 (fp32 4.3 against 5.0); 2048: 4.8 against 4.0
-//   one choice, and two of words wider than 1024, one: T = 8192, k = 2: 36 / 38 against 50
+// of groups of 1 / 2 / 4 / 8 and of a block per token (bf16 rows, H = 2048 unless it says otherwise; inputs
+// that change from pass to pass):
+//   up to 1024 pairs, where latency counts, one choice: T = 1, k = 8: 1.6 against 2.8 per token; 512 pairs:
+//     3.1 against 4.8; 1024: 3.9 against 5.2; 2048: 6.3 each
+//   one choice, and two of words wider than 1024, one: T = 8192, k = 2: 36 / 39 / 40 / 70 against 50
 //   single values, bound by their loads and stores, of which a group shares dout's, four (two of two):
-//     T = 2048, k = 8: 48 / 42 / 36 / 42; H = 1031: 32 / 26 / 22; T = 4096, H = 255: 34 / 17 / 9.1 / 8.4
-//   two narrow choices of words, two: T = 8192, H = 512: 17 / 8.9 against 10
-//   fp32 words from 512 values on, two: T = 2048, k = 8: 51 / 45 / 46 / 51 against 54; k = 4: 27 / 24 / 25 /
-//     29 against 30; T = 4096, k = 8, H = 512: 35 / 23 / 23 / 25 against 29 (H = 128: 34 / 17 / 8.9 / 6.1
-//     against 8.1)
-//   other words, a block per token: T = 2048, k = 8: 35 / 37 / 32 / 43 against 27
+//     T = 2048, k = 8: 49 / 42 / 37 / 42; H = 1031: 39 / 35 / 29 / 35; T = 4096, H = 255: 34 / 18 / 13 / 12
+//   two narrow choices of words, two: T = 8192, H = 512: 17 / 12 / 12 / 17 against 14
+//   fp32 words from 512 values on, two: T = 2048, k = 8: 51 / 45 / 47 / 51 against 54; k = 4: 27 / 25 / 27 /
+//     29 against 31; T = 4096, k = 8, H = 512: 34 / 24 / 25 / 26 against 29; below, H = 256: 34 / 17 / 14 / 14
+//     against 18, H = 128: 34 / 17 / 11 / 10 against 8.9
+//   other words, a block per token: T = 2048, k = 8: 35 / 37 / 32 / 44 against 27; k = 4: 19 / 20 / 19 / 28
+//     against 18; k = 3: 15 / 18 / 16 / 24 against 16
 template <typename YT, typename OT, int NT, int G>
 __global__ void __launch_bounds__(kRowThreads)
     combine_group_backward_kernel(const OT* __restrict__ dout, int64_t ldo, const YT* __restrict__ yp, int64_t ldy,

@@ -7,6 +7,9 @@
 // (e = 0..7): single values, neighbouring threads on neighbouring addresses, any H and any stride. (As a
 // constant it makes the addresses of a row's values offsets of one pointer: 2 to 4 instructions per
 // value read, not 20.) Values past H read as 0 and are not written.
+//
+// Times in the comments of these files rank two forms of a kernel against each other, most of them on inputs
+// that repeat from pass to pass, so that inputs below some 100 MB were in L2.
 #pragma once
 
 #include <cuda_fp16.h>
