@@ -99,7 +99,10 @@ struct GParams {
   int* ctl;
 };
 
-// packed tile: expert (8 bits) | chunk (12 bits) | block pair (12 bits)
+// packed tile: expert (8 bits) | chunk (12 bits) | block pair (12 bits); experts from 128 on set the sign
+// bit. kNoTile ends the queue: the fields of a tile are never all ones (4095 chunks and 4095 block pairs
+// at most, see ffn_grouped_supported).
+constexpr int32_t kNoTile = -1;
 __device__ __forceinline__ void unpack_tile(int32_t v, int& e, int& chunk, int& bp) {
   e = (v >> 24) & 0xff;
   chunk = (v >> 12) & 0xfff;
@@ -261,7 +264,7 @@ grouped_gemm_kernel(const __grid_constant__ GParams P, const __grid_constant__ B
         break;
       }
       if (lane == 0) {
-        s.tq[q] = stop ? -1 : P.tile_list[t];
+        s.tq[q] = stop ? kNoTile : P.tile_list[t];
         tc::mbar_arrive(&s.tq_full[q]);
       }
       if (stop) break;
@@ -332,7 +335,7 @@ grouped_gemm_kernel(const __grid_constant__ GParams P, const __grid_constant__ B
         if (!tc::mbar_wait(&s.tq_full[q], (n >> 2) & 1, abort)) { report_status(P.ctl, MOE_ERR_TIMEOUT, 23); break; }
         const int packed = s.tq[q];
         tc::mbar_arrive(&s.tq_empty[q]);
-        if (packed < 0) break;
+        if (packed == kNoTile) break;
         const TileDesc d = describe(P, packed);
         const int nmma = (d.ntok + 15) & ~15;
         const uint32_t idesc = tc::idesc_bf16_f32(128, nmma);
@@ -403,7 +406,7 @@ grouped_gemm_kernel(const __grid_constant__ GParams P, const __grid_constant__ B
       const int packed = s.tq[q];
       __syncwarp();
       if (lane == 0) tc::mbar_arrive(&s.tq_empty[q]);
-      if (packed < 0) break;
+      if (packed == kNoTile) break;
       int bp = packed & 0xfff, g0, g1, part;
       k_range(P, bp, g0, g1, part);
       bool ok = true;
@@ -460,7 +463,7 @@ grouped_gemm_kernel(const __grid_constant__ GParams P, const __grid_constant__ B
       const int packed = s.tq[q];
       __syncwarp();
       if (lane == 0) tc::mbar_arrive(&s.tq_empty[q]);
-      if (packed < 0) break;
+      if (packed == kNoTile) break;
       const TileDesc d = describe(P, packed);
       if (!bar_and(1, 128, gwait(&s.dfull, n & 1, abort))) break;
       tc::tc_fence_after();
@@ -566,7 +569,7 @@ __global__ void __launch_bounds__(256) tile_list_kernel(const int32_t* __restric
   __syncthreads();
   for (int i = threadIdx.x; i < mine; i += blockDim.x) {
     const int chunk = i / pairs, bp = i % pairs;
-    list[base + i] = (e << 24) | (chunk << 12) | bp;
+    list[base + i] = (int32_t)((uint32_t)e << 24 | (uint32_t)chunk << 12 | (uint32_t)bp);
   }
 }
 
