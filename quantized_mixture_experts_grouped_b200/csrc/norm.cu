@@ -424,9 +424,9 @@ int check_ld(const char* me, const char* name, const void* p, int64_t ld, int T,
   return MOE_OK;
 }
 
-int check_gate(const char* me, const void* gate, int mode) {
+int check_gate(const char* me, const void* gate, int mode, int T) {
   if (mode < MOE_GATE_NONE || mode > MOE_GATE_FULL) return fail(MOE_ERR_ARG, "%s: unknown gate mode %d", me, mode);
-  if ((mode != MOE_GATE_NONE) != (gate != nullptr))
+  if (T > 0 && (mode != MOE_GATE_NONE) != (gate != nullptr))
     return fail(MOE_ERR_ARG, "%s: gate pointer and gate mode %d do not go together", me, mode);
   return MOE_OK;
 }
@@ -467,7 +467,7 @@ int launch_post(const PostArgs& a, int rows, bool vec, cudaStream_t s) {
 int check_post(const char* me, const PostArgs& a, int T, int H, int dtype, int flags, bool* vec) {
   if (int rc = check_norm(me, T, H, dtype, a.eps)) return rc;
   if (flags & ~(MOE_NORM_Y | MOE_NORM_NEXT)) return fail(MOE_ERR_ARG, "%s: unknown flags %d", me, flags);
-  if (int rc = check_gate(me, a.gate, a.gate_mode)) return rc;
+  if (int rc = check_gate(me, a.gate, a.gate_mode, T)) return rc;
   if (T > 0 && (!a.y || !a.h || !a.h_out || (a.next && !a.x_next))) return fail(MOE_ERR_ARG, "%s: null pointer", me);
   if (T > 0 && ((a.h_out == a.h && a.ldho != a.ldh) || a.h_out == a.y ||
                 (a.next && (a.x_next == a.h_out || a.x_next == a.h || a.x_next == a.y))))
@@ -689,7 +689,7 @@ MOE_API int moe_norm_post_backward(const void* dh_out, int64_t dh_out_stride, co
   const char* me = "moe_norm_post_backward";
   if (int rc = check_norm(me, T, H, dtype, eps)) return rc;
   if (flags & ~(MOE_NORM_Y | MOE_NORM_NEXT)) return fail(MOE_ERR_ARG, "%s: unknown flags %d", me, flags);
-  if (int rc = check_gate(me, gate, gate_mode)) return rc;
+  if (int rc = check_gate(me, gate, gate_mode, T)) return rc;
   const bool norm_y = flags & MOE_NORM_Y, next = flags & MOE_NORM_NEXT;
   if (T > 0 && (!dh_out || !y || !dh || !dy || (next && (!h_out || !dx_next))))
     return fail(MOE_ERR_ARG, "%s: null pointer", me);

@@ -677,7 +677,7 @@ MOE_API int moe_combine_backward(const void* dout, int64_t dout_stride, int dout
   if (int rc = check_dtype(me, dout_dtype)) return rc;
   if (yp_dtype != dout_dtype && yp_dtype != MOE_DTYPE_F32)
     return fail(MOE_ERR_ARG, "%s: rows of type %d with results of type %d", me, yp_dtype, dout_dtype);
-  if (!dyp && !dwts) return fail(MOE_ERR_ARG, "%s: dyp and dwts are both null", me);
+  if (T > 0 && !dyp && !dwts) return fail(MOE_ERR_ARG, "%s: dyp and dwts are both null", me);
   if (T > 0 && (!dout || !inv || !wts || (dwts && !yp))) return fail(MOE_ERR_ARG, "%s: null pointer", me);
   if (dyp && (dyp == yp || dyp == dout)) return fail(MOE_ERR_ARG, "%s: dyp overlaps an input", me);
   if (int rc = check_stride(me, "dout", dout_stride, T, H, false)) return rc;

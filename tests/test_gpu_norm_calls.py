@@ -120,3 +120,25 @@ def test_pre_of_many_rows(res, T, H, pad, dt, monkeypatch):
     on_device(dw, rw, bw, "dw")
     q.moe_norm_pre_backward(dx, h, w, EPS, d2, dres=dres)
     assert torch.equal(d2, dh)
+
+
+@pytest.mark.parametrize("gate", ["none", "channel", "token", "full"])
+def test_no_tokens(gate):
+    """An empty batch with every kind of gate and all gradients: vectors' gradients are zeros."""
+    T, H, k, E = 0, 64, 2, 8
+    e = lambda *s, dt=torch.bfloat16: torch.empty(s, dtype=dt, device="cuda")
+    i32, f32 = torch.int32, torch.float32
+    gt = {"none": None, "channel": torch.ones(H, dtype=torch.bfloat16, device="cuda"), "token": e(T, 1, dt=f32),
+          "full": e(T, H)}[gate]
+    dg = {"none": None, "channel": torch.ones(H, device="cuda"), "token": e(T, dt=f32), "full": e(T, H)}[gate]
+    dw, dn = torch.ones(H, device="cuda"), torch.ones(H, device="cuda")
+    q.moe_norm_post(e(T, H), e(T, H), e(T, H), EPS, gate=gt, x_next=e(T, H))
+    q.moe_combine_norm_post(e(T * k, H), e(T, k, dt=i32), e(T, k, dt=f32), e(T, H), e(T, H), EPS, gate=gt,
+                            x_next=e(T, H), y_out=e(T, H))
+    q.moe_norm_post_backward(e(T, H), e(T, H), e(T, H), e(T, H), EPS, dw=dw, gate=gt, dgate=dg, h_out=e(T, H),
+                             dx_next=e(T, H), dw_next=dn)
+    assert (dw == 0).all() and (dn == 0).all() and (gate != "channel" or (dg == 0).all())
+    q.moe_combine(e(T * k, H), e(T, k, dt=i32), e(T, k, dt=f32), e(T, H))
+    q.moe_combine_backward(e(T, H), e(T * k, H), e(T, k, dt=i32), e(T, k, dt=f32), e(T * k, H), e(T, k, dt=f32))
+    q.moe_dispatch_backward(e(T * k, H), e(T, k, dt=i32), e(T, H))
+    q.moe_route_topk_backward(e(T, k, dt=i32), e(T, k, dt=f32), e(T, k, dt=f32), e(T, E))

@@ -209,3 +209,24 @@ def test_fused(change, code, says):
     (dict(ws=ctypes.c_void_p((1 << 40) + 128)), ARG, "aligned")])
 def test_post_backward(change, code, says):
     refused("moe_norm_post_backward", BACK, BACK_BASE, change, code, says)
+
+
+def test_no_tokens_and_no_buffers():
+    """An empty batch's tensors have no address: the calls are valid and launch nothing."""
+    def ok(fn, order, base, **change):
+        args = {**base, "T": 0, **change}
+        assert getattr(q.lib, fn)(*(args[n] for n in order.split()), None) == q.MOE_OK, (
+            fn, q.lib.moe_last_error_string())
+    rows = "yp inv wts out dout dyp dwts idx dl h x y ho xn yo dho dh dy dx dxp dres"
+    none = {n: N for n in rows.split()}
+    ok("moe_dispatch_backward", "dxp ld dt inv T H k dx ld", none, ld=8, dt=BF16, H=8, k=2)
+    ok("moe_combine", "yp ld dt inv wts T H k out ld dt", none, ld=8, dt=BF16, H=8, k=2)
+    ok("moe_combine_backward", "dout ld dt yp ld dt inv wts T H k dyp ld dwts", none, ld=8, dt=BF16, H=8, k=2)
+    ok("moe_route_topk_backward", "idx wts dwts T E k dl ld dt", none, E=8, k=2, ld=8, dt=F32)
+    ok("moe_norm_pre", PRE, {**none, "w": N}, ldh=8, dt=BF16, eps=1e-5, H=8, ldx=8)
+    ok("moe_norm_pre_backward", PRE_BACK, {**none, "w": N, "dw": N, "ws": N}, lddx=8, ldh=8, dt=BF16, eps=1e-5,
+       H=8, ldr=8, lddh=8, wb=0)
+    for mode in (0, 2, 3):                      # a gate per token or per value is empty too
+        ok("moe_norm_post", POST, {**POST_BASE, **none, "gate": N}, mode=mode)
+        ok("moe_combine_norm_post", FUSED, {**FUSED_BASE, **none, "gate": N}, mode=mode)
+        ok("moe_norm_post_backward", BACK, {**BACK_BASE, **none, "gate": N, "dg": N, "dw": N, "dwn": N}, mode=mode)
