@@ -275,8 +275,11 @@ int moe_combine_backward(const void* dout, int64_t dout_stride, int dout_dtype,
 
 /* Gradient of moe_route_topk's weights towards the logits. The renormalised weights are a softmax
  * over the k chosen logits, so dlogits[t][idx_j] = w_j * (dwts_j - sum_i w_i * dwts_i), and 0 for
- * every expert not chosen. idx, wts: the router's outputs [T][k] (an id outside [0, E) is not
- * written but counts in the sum; an id given twice adds up). dlogits: [T][E], dtype MOE_DTYPE_*.
+ * every expert not chosen. idx, wts: the router's own outputs [T][k] (an id outside [0, E) is not
+ * written but counts in the sum; an id given twice adds up). Where choices were dropped after the
+ * router (-1 in the ids given to moe_dispatch), give the ids as they were before: a dropped choice has
+ * dwts_j = 0, but its logit still has the gradient -w_j * sum_i w_i * dwts_i, and an id of -1 loses
+ * it. dlogits: [T][E], dtype MOE_DTYPE_*.
  * Errors: MOE_ERR_ARG, MOE_ERR_SHAPE (E > 256). */
 int moe_route_topk_backward(const int32_t* idx, const float* wts, const float* dwts,
                             int T, int E, int k, void* dlogits, int64_t dlogits_stride, int dtype,

@@ -260,7 +260,8 @@ def moe_combine_backward(dout, yp, inv, wts, dyp=None, dwts=None, stream=None):
 
 
 def moe_route_topk_backward(idx, wts, dwts, dlogits, stream=None):
-    """Gradient of moe_route_topk's weights towards the logits: dlogits [T][E], 0 where not chosen."""
+    """Gradient of moe_route_topk's weights towards the logits: dlogits [T][E], 0 where not chosen. idx: the
+    router's own ids, also of choices dropped after it (their logits have a gradient too)."""
     _rows.route_topk_backward(idx, wts, dwts, dlogits, stream)
 
 

@@ -57,3 +57,34 @@ def test_most_tokens():
     assert all_are(3.0)
     q.moe_route_topk_backward(zeros, ones, ones, out)          # 1 * (1 - 1 * 1)
     assert all_are(0.0)
+
+
+def test_router_gradient_with_dropped_choices():
+    """Choices dropped after the router, by -1 in a copy of its ids: with the router's own ids the logits'
+    gradient is autograd's, a dropped choice's logit included."""
+    import rows_ref as ref
+    g = torch.Generator().manual_seed(14)
+    T, E, k, H = 40, 16, 4, 64
+    logits = torch.randn((T, E), generator=g).bfloat16()
+    idx, wts = torch.empty((T, k), dtype=torch.int32, device="cuda"), torch.empty((T, k), device="cuda")
+    q.moe_route_topk(logits.cuda(), k, idx, wts)
+    kept = torch.where(torch.rand((T, k), generator=g).cuda() < 0.3, -1, idx)
+    x, dout = torch.randn((T, H), generator=g).cuda(), torch.randn((T, H), generator=g).cuda()
+    i32 = dict(dtype=torch.int32, device="cuda")
+    inv, xp = torch.empty((T, k), **i32), torch.zeros((T * k, H), device="cuda")
+    q.moe_dispatch(x, kept, E, torch.empty(E, **i32), torch.empty(E + 1, **i32), torch.empty(T * k, **i32), inv, xp)
+    scale = torch.randn(T * k, 1, generator=g).cuda()        # the experts: a factor of each row
+    yp, dwts, dlogits = xp * scale, torch.empty_like(wts), torch.empty((T, E), device="cuda")
+    q.moe_combine_backward(dout, yp, inv, wts, dwts=dwts)
+    q.moe_route_topk_backward(idx, wts, dwts, dlogits)
+    z = logits.double().requires_grad_()
+    w = torch.softmax(z.gather(1, idx.cpu().long()), 1)
+    rows = torch.where((inv >= 0)[:, :, None], yp[inv.clamp(min=0).long()], 0.0).cpu().double()
+    ((w[:, :, None] * rows).sum(1) * dout.cpu().double()).sum().backward()
+    # weights within 2e-6 relative, products of H terms within H * 2^-24 of their absolute sum
+    mag = (rows.abs() * dout.cpu().double().abs()[:, None]).sum(2)
+    part = w.detach() * (mag + (w.detach() * mag).sum(1, keepdim=True))
+    bound = torch.zeros_like(z).scatter_(1, idx.cpu().long(), part * (4 * 2e-6 + H * 2.0 ** -24))
+    ref.check(dlogits, z.grad, bound.detach())
+    gone = (kept < 0).cpu()
+    assert gone.any() and (dlogits.cpu().gather(1, idx.cpu().long())[gone] != 0).any()
