@@ -631,8 +631,10 @@ MOE_API int moe_dispatch(const void* x, int64_t x_stride, int dtype, const int32
   if (!counts || !offsets || (T > 0 && (!x || !idx || !perm || !inv || !xp)))
     return fail(MOE_ERR_ARG, "%s: null pointer", me);
   if (T > 0 && x == xp) return fail(MOE_ERR_ARG, "%s: xp overlaps x", me);
-  if (T > 0 && (idx == inv || idx == perm || inv == perm || idx == counts || idx == offsets))
-    return fail(MOE_ERR_ARG, "%s: idx and the index outputs overlap", me);
+  const void* ints[] = {counts, offsets, perm, inv, idx};      // an empty batch has only the first two
+  for (int i = 0, n = T > 0 ? 5 : 2; i < n; ++i)
+    for (int j = 0; j < i; ++j)
+      if (ints[i] == ints[j]) return fail(MOE_ERR_ARG, "%s: idx and the index outputs overlap", me);
   if (int rc = check_stride(me, "x", x_stride, T, H, false)) return rc;
   if (int rc = check_stride(me, "xp", xp_stride, (int64_t)T * k, H, true)) return rc;
   return launch_dispatch(x, x_stride, dtype_size(dtype), idx, T, H, E, k, counts, offsets, perm, inv, xp, xp_stride,

@@ -102,7 +102,9 @@ DISPATCH_BASE = dict(buffers("x idx counts offsets perm inv xp"), ldx=8, dt=BF16
     (dict(ldp=0), ARG, "row stride 0 of xp"), (dict(xp="x"), ARG, "xp overlaps x"),
     (dict(T=1 << 30, k=4), SHAPE, "T*k"), (dict(H=(1 << 30) + 1, ldp=1 << 31), SHAPE, "2^30"),
     *[({n: "idx"}, ARG, "index outputs overlap") for n in ("counts", "offsets", "perm", "inv")],
-    (dict(perm="inv"), ARG, "index outputs overlap")])
+    *[({a: b}, ARG, "index outputs overlap") for a, b in (("perm", "inv"), ("counts", "offsets"), ("counts", "perm"),
+                                                           ("counts", "inv"), ("offsets", "perm"), ("offsets", "inv"))],
+    (dict(T=0, counts="offsets"), ARG, "index outputs overlap")])
 def test_dispatch(change, code, says):
     refused("moe_dispatch", DISPATCH, DISPATCH_BASE, change, code, says)
 
